@@ -140,7 +140,8 @@ typedef enum {
     MHC_OP_PROJ_RMS_PARTIAL_FWD = 9,   /* C = the shard's channels Cs */
     MHC_OP_COMPUTE_H_BWD = 10,
     MHC_OP_PROJ_RMS_PARTIAL_BWD = 11,  /* C = the shard's channels Cs */
-    MHC_OP_H_POST_BDA_COMPUTE_H_FWD = 12
+    MHC_OP_H_POST_BDA_COMPUTE_H_FWD = 12,
+    MHC_OP_QK_NORM_ROPE_BWD = 13 /* (T, Hq + Hk, D); only when a dgamma is wanted */
 } mhc_op;
 
 /* Workspace bytes an op needs for (T, n, C); 0 for a bad op or shape.
@@ -403,6 +404,135 @@ MHC_API mhc_status mhc_h_post_bda_compute_h_fwd(
     int64_t T, int n, int64_t C, int iters, float eps_sk, float eps_rms, mhc_bf16 *out,
     float *H_pre_next, float *H_post_next, float *H_res_next, float *u_save_next,
     float *r_save_next, void *ws, size_t ws_bytes, mhc_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* The edges of the sub-layers that the residual path wraps: the entry  */
+/* of attention (norm of queries and keys per head with the position    */
+/* rotation), and a mixture of experts (router, sort of the token slots */
+/* by expert, rows to the experts and back), forward and backward.      */
+/* The web pages have no counterpart of these entry points.             */
+/*                                                                      */
+/* Their activations are bf16, fp16 or fp32 (`dtype`, one for all of a  */
+/* call's activations); arithmetic and sums are fp32, and each result   */
+/* is rounded to the activation type once.  Parameter gradients,        */
+/* router weights and tables are fp32, indices int32.                   */
+/* A bad index in device memory cannot be refused on the host: the      */
+/* kernels check each before they use it, leave it out and set the      */
+/* device error word (201 a position outside the table, 202 an expert   */
+/* outside [-1, E) in mhc_moe_sort, 203 a row outside [-1, R), 204 an   */
+/* expert outside [-1, E) in mhc_moe_router_bwd).                       */
+/* A token's results do not depend on T or on its place in the batch.   */
+/* ------------------------------------------------------------------ */
+
+typedef enum { MHC_BF16 = 0, MHC_FP16 = 1, MHC_FP32 = 2 } mhc_dtype;
+
+#define MHC_MAX_HEAD_DIM 512
+
+/* Per head h of q [T, Hq, D] and k [T, Hk, D]:
+ *   rho = (sum_d x_d^2 / D + eps)^-1/2,  a = x rho gamma   (an all-zero head
+ *   with eps = 0 gives zeros), then for the R/2 pairs p of the first R
+ *   elements, (i, j) = (p, p + R/2), or (2p, 2p + 1) if interleaved:
+ *   y_i = a_i cos[pos][p] - a_j sin[pos][p],  y_j = a_j cos[pos][p] + a_i sin[pos][p];
+ *   y = a for the elements past R.
+ * gamma_q, gamma_k [D] fp32 (NULL: 1); cos, sin [P, R/2] fp32; pos [T] int32,
+ * each in [0, P) (NULL: pos = t, T <= P); 1 <= D <= 512, 0 <= R <= D even
+ * (R = 0: no rotation; cos, sin unused).  A token whose position is outside
+ * the table gets zeros (device error 201).
+ * strides: 8 element strides in HOST memory, (token, head) of q, k, q_out,
+ * k_out in this order, or NULL: all contiguous [T, H, D].  The D elements of
+ * a head are contiguous.  q, k, q_out, k_out and pos need only the alignment
+ * of their elements; 16-byte pointers and strides, D a multiple of 8 and R of
+ * 16 take the fastest path.  q_out may be q and k_out k (same strides);
+ * outputs must not overlap inputs otherwise.  Hq or Hk may be 0. */
+MHC_API mhc_status mhc_qk_norm_rope_fwd(const void *q, const void *k, mhc_dtype dtype,
+                                        const int64_t *strides, const float *gamma_q,
+                                        const float *gamma_k, const float *cos, const float *sin,
+                                        const int32_t *pos, int64_t T, int Hq, int Hk, int D,
+                                        int R, int64_t P, int interleaved, float eps, void *q_out,
+                                        void *k_out, mhc_stream_t stream);
+
+/* The gradient, from the inputs q, k of the forward:  b = the inverse
+ * rotation of the upstream gradient, g = b gamma, xh = x rho:
+ *   dx = rho (g - xh (sum_d g xh) / D),  dgamma[d] = sum over tokens and
+ * heads of b_d xh_d (fp32, fixed order; dgamma_q, dgamma_k may be NULL).
+ * strides: 12, (token, head) of dq_out, dk_out, q, k, dq, dk, or NULL.
+ * dq may be dq_out or q, dk dk_out or k (same strides).  With T = 0 the
+ * dgamma are zeroed.
+ * ws: mhc_workspace_bytes(MHC_OP_QK_NORM_ROPE_BWD, T, Hq + Hk, D), only when
+ * a dgamma is wanted. */
+MHC_API mhc_status mhc_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
+                                        const void *k, mhc_dtype dtype, const int64_t *strides,
+                                        const float *gamma_q, const float *gamma_k,
+                                        const float *cos, const float *sin, const int32_t *pos,
+                                        int64_t T, int Hq, int Hk, int D, int R, int64_t P,
+                                        int interleaved, float eps, void *dq, void *dk,
+                                        float *dgamma_q, float *dgamma_k, void *ws,
+                                        size_t ws_bytes, mhc_stream_t stream);
+
+#define MHC_MOE_MAX_EXPERTS 1024
+#define MHC_MOE_MAX_K 32
+#define MHC_MOE_MAX_ALIGN 65536
+
+typedef enum { MHC_SCORE_SOFTMAX = 0, MHC_SCORE_SIGMOID = 1 } mhc_score;
+
+/* ids [T, k] int32 of each token's k largest logits [T, E], in descending
+ * order, ties to the lowest index (the logits are compared as stored; NaN
+ * ranks above all), and their weights w [T, k] fp32:
+ *   softmax:  scale p over all E logits;  renorm: scale softmax over the chosen;
+ *   sigmoid:  scale s(l);  renorm: scale s(l) / sum of the chosen s.
+ * -inf masks an expert; a row with nothing left has weights 0.
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32). */
+MHC_API mhc_status mhc_moe_router_fwd(const void *logits, mhc_dtype dtype, int64_t T, int E,
+                                      int k, mhc_score score, int renorm, float scale,
+                                      int32_t *ids, float *w, mhc_stream_t stream);
+
+/* dlogits [T, E] (type of the logits) from dw [T, k] fp32, the logits and
+ * ids of the forward; an id of -1 (a dropped slot) carries no gradient. */
+MHC_API mhc_status mhc_moe_router_bwd(const float *dw, const void *logits, mhc_dtype dtype,
+                                      const int32_t *ids, int64_t T, int E, int k,
+                                      mhc_score score, int renorm, float scale, void *dlogits,
+                                      mhc_stream_t stream);
+
+/* Rows that the sorted slots of T tokens can take: T*k, and align - 1 for
+ * each of min(E, T*k) experts; -1 for arguments out of range. */
+MHC_API int64_t mhc_moe_rows(int64_t T, int k, int E, int align);
+
+/* Stable sort of the T*k slots (slot t*k + j) by expert.  ids [T, k] int32 in
+ * [-1, E), -1 a dropped slot (any other value outside is dropped too and sets
+ * device error 202).  counts [E]: slots of each expert; offsets [E + 1]: its
+ * first row, each segment rounded up to `align` rows (1 <= align <= 65536),
+ * offsets[E] the rows in use; row_of [T, k]: a slot's row, -1 if dropped;
+ * slot_of [R]: a row's slot, -1 for padding and for the rows past
+ * offsets[E].  mhc_moe_rows(T, k, E, align) <= R < 2^31.  T may be 0 (counts,
+ * offsets and slot_of are still written). */
+MHC_API mhc_status mhc_moe_sort(const int32_t *ids, int64_t T, int k, int E, int align,
+                                int64_t R, int32_t *counts, int32_t *offsets, int32_t *row_of,
+                                int32_t *slot_of, mhc_stream_t stream);
+
+/* xs [R, C]: xs[row_of[t][j]] = x[t]; the rows without a slot are zeroed.
+ * C a multiple of 8. */
+MHC_API mhc_status mhc_moe_dispatch_fwd(const void *x, mhc_dtype dtype, const int32_t *row_of,
+                                        const int32_t *slot_of, int64_t T, int k, int64_t R,
+                                        int64_t C, void *xs, mhc_stream_t stream);
+
+/* dx [T, C]: dx[t] = sum_j dxs[row_of[t][j]] (dropped slots add nothing). */
+MHC_API mhc_status mhc_moe_dispatch_bwd(const void *dxs, mhc_dtype dtype, const int32_t *row_of,
+                                        int64_t T, int k, int64_t R, int64_t C, void *dx,
+                                        mhc_stream_t stream);
+
+/* f [T, C]: f[t] = sum_j w[t][j] ys[row_of[t][j]], j ascending; w [T, k]
+ * fp32, NULL: 1.  Rows without a slot are not read. */
+MHC_API mhc_status mhc_moe_combine_fwd(const void *ys, mhc_dtype dtype, const float *w,
+                                       const int32_t *row_of, int64_t T, int k, int64_t R,
+                                       int64_t C, void *f, mhc_stream_t stream);
+
+/* dys [R, C]: dys[row_of[t][j]] = w[t][j] df[t], rows without a slot zeroed;
+ * dw [T, k] fp32: dw[t][j] = sum_c df[t][c] ys[row_of[t][j]][c], 0 for a
+ * dropped slot.  dw may be NULL (ys is then not read). */
+MHC_API mhc_status mhc_moe_combine_bwd(const void *df, const void *ys, mhc_dtype dtype,
+                                       const float *w, const int32_t *row_of,
+                                       const int32_t *slot_of, int64_t T, int k, int64_t R,
+                                       int64_t C, void *dys, float *dw, mhc_stream_t stream);
 
 /* ------------------------------------------------------------------ */
 /* Per-kernel timing (off by default).  When enabled, every kernel the  */

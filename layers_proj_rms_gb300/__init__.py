@@ -30,6 +30,9 @@ __all__ = [
     "OP_PROJ_RMS_PARTIAL_BWD", "mhc_set_batch_invariant", "mhc_batch_invariant",
     "mhc_set_pinned_reductions", "mhc_pinned_reductions",
     "mhc_h_post_bda_compute_h_fwd", "OP_H_POST_BDA_COMPUTE_H_FWD", "mhc_selftest_wait_timeout",
+    "mhc_qk_norm_rope_fwd", "mhc_qk_norm_rope_bwd", "OP_QK_NORM_ROPE_BWD", "mhc_moe_router_fwd",
+    "mhc_moe_router_bwd", "SCORE_SOFTMAX", "SCORE_SIGMOID", "mhc_moe_rows", "mhc_moe_sort",
+    "mhc_moe_dispatch_fwd", "mhc_moe_dispatch_bwd", "mhc_moe_combine_fwd", "mhc_moe_combine_bwd",
 ]
 
 

@@ -29,6 +29,10 @@ OP_PROJ_RMS_PARTIAL_FWD = 9
 OP_COMPUTE_H_BWD = 10
 OP_PROJ_RMS_PARTIAL_BWD = 11
 OP_H_POST_BDA_COMPUTE_H_FWD = 12
+OP_QK_NORM_ROPE_BWD = 13
+
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -72,6 +76,17 @@ _SIGS = {
     "mhc_proj_rms_partial_bwd": [_P, _P, _P, _P, _I64, _I, _I64, _P, _P, _P, _SZ, _P],
     "mhc_h_post_bda_compute_h_fwd": [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I, _I64, _I, _F, _F,
                                      _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+    "mhc_qk_norm_rope_fwd": [_P, _P, _I, _P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I, _I64, _I,
+                             _F, _P, _P, _P],
+    "mhc_qk_norm_rope_bwd": [_P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _P, _I64, _I, _I, _I, _I,
+                             _I64, _I, _F, _P, _P, _P, _P, _P, _SZ, _P],
+    "mhc_moe_router_fwd": [_P, _I, _I64, _I, _I, _I, _I, _F, _P, _P, _P],
+    "mhc_moe_router_bwd": [_P, _P, _I, _P, _I64, _I, _I, _I, _I, _F, _P, _P],
+    "mhc_moe_sort": [_P, _I64, _I, _I, _I, _I64, _P, _P, _P, _P, _P],
+    "mhc_moe_dispatch_fwd": [_P, _I, _P, _P, _I64, _I, _I64, _I64, _P, _P],
+    "mhc_moe_dispatch_bwd": [_P, _I, _P, _I64, _I, _I64, _I64, _P, _P],
+    "mhc_moe_combine_fwd": [_P, _I, _P, _P, _I64, _I, _I64, _I64, _P, _P],
+    "mhc_moe_combine_bwd": [_P, _P, _I, _P, _P, _P, _I64, _I, _I64, _I64, _P, _P, _P],
 }
 for _name, _args in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -93,6 +108,8 @@ lib.mhc_pinned_reductions.argtypes = []
 lib.mhc_pinned_reductions.restype = ctypes.c_int
 lib.mhc_workspace_bytes.argtypes = [_I, _I64, _I, _I64]
 lib.mhc_workspace_bytes.restype = ctypes.c_size_t
+lib.mhc_moe_rows.argtypes = [_I64, _I, _I, _I]
+lib.mhc_moe_rows.restype = ctypes.c_int64
 
 
 class MhcError(RuntimeError):
@@ -432,6 +449,177 @@ def mhc_proj_rms_partial_bwd(x_shard, W_shard, du, coef, dx_shard, dW_shard, ws,
         _ptr(du, _F32, (T, O), "du"), _ptr(coef, _F32, (T,), "coef"), T, n, Cs,
         _ptr(dx_shard, _BF, (T, n, Cs), "dx_shard"), _ptr(dW_shard, _F32, (n * Cs, O), "dW_shard"),
         wp, wb, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# the entry of attention, mixture of experts
+# ---------------------------------------------------------------------------
+
+_I32 = torch.int32
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _act(t, name):
+    """The library's code of an activation tensor's dtype."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16, float16 or float32")
+    return code
+
+
+def _act_ptr(t, name):
+    code = _act(t, name)
+    return _ptr(t, name=name), code
+
+
+def _heads(t, dtype, shape, name):
+    """Pointer and (token, head) strides of a [T, H, D] tensor or view."""
+    if t is None and not shape[1]:
+        return None, (0, 0)
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    st = t.stride()
+    if st[2] != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if not t.numel():
+        return None, (0, 0)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.data_ptr(), st[:2]
+
+
+def _qk_shapes(q, k, cos, sin):
+    for t, name in ((q, "q"), (k, "k")):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 3):
+            raise ValueError(f"{name} must be a [T, H, D] tensor")
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q and k are both None")
+    code = _act(one, "q" if q is not None else "k")
+    T, _, D = one.shape
+    sq = (T, q.shape[1] if q is not None else 0, D)
+    sk = (T, k.shape[1] if k is not None else 0, D)
+    if cos is None:
+        return code, one.dtype, sq, sk, 0, 0
+    P, half = cos.shape
+    return code, one.dtype, sq, sk, 2 * half, P
+
+
+def mhc_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, cos, sin, pos, eps, q_out, k_out,
+                         interleaved=False, stream=None):
+    """q [T, Hq, D], k [T, Hk, D] and the outputs may be views with any token
+    and head strides (slices of a packed qkv product, [H, T, D] layouts);
+    q or k may be None; cos and sin None: no rotation."""
+    code, dt, sq, sk, R, P = _qk_shapes(q, k, cos, sin)
+    T, Hq, D = sq
+    pq, a = _heads(q, dt, sq, "q")
+    pk, b = _heads(k, dt, sk, "k")
+    oq, c = _heads(q_out, dt, sq, "q_out")
+    ok, d = _heads(k_out, dt, sk, "k_out")
+    _ok(lib.mhc_qk_norm_rope_fwd(
+        pq, pk, code, _S8(*a, *b, *c, *d),
+        _ptr(gamma_q, _F32, (D,), "gamma_q"), _ptr(gamma_k, _F32, (D,), "gamma_k"),
+        _ptr(cos, _F32, (P, R // 2), "cos"), _ptr(sin, _F32, (P, R // 2), "sin"),
+        _ptr(pos, _I32, (T,), "pos"), T, Hq, sk[1], D, R, P, interleaved, eps, oq, ok,
+        _stream(stream)))
+
+
+def mhc_qk_norm_rope_bwd(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, pos, eps, dq, dk,
+                         dgamma_q=None, dgamma_k=None, ws=None, interleaved=False, stream=None):
+    code, dt, sq, sk, R, P = _qk_shapes(q, k, cos, sin)
+    T, Hq, D = sq
+    pu, a = _heads(dq_out, dt, sq, "dq_out")
+    pv, b = _heads(dk_out, dt, sk, "dk_out")
+    pq, c = _heads(q, dt, sq, "q")
+    pk, d = _heads(k, dt, sk, "k")
+    oq, e = _heads(dq, dt, sq, "dq")
+    ok, f = _heads(dk, dt, sk, "dk")
+    wp, wb = _ws(ws)
+    _ok(lib.mhc_qk_norm_rope_bwd(
+        pu, pv, pq, pk, code, _S12(*a, *b, *c, *d, *e, *f),
+        _ptr(gamma_q, _F32, (D,), "gamma_q"), _ptr(gamma_k, _F32, (D,), "gamma_k"),
+        _ptr(cos, _F32, (P, R // 2), "cos"), _ptr(sin, _F32, (P, R // 2), "sin"),
+        _ptr(pos, _I32, (T,), "pos"), T, Hq, sk[1], D, R, P, interleaved, eps, oq, ok,
+        _ptr(dgamma_q, _F32, (D,), "dgamma_q"), _ptr(dgamma_k, _F32, (D,), "dgamma_k"), wp, wb,
+        _stream(stream)))
+
+
+_S8 = ctypes.c_int64 * 8
+_S12 = ctypes.c_int64 * 12
+
+
+def mhc_moe_router_fwd(logits, score, renorm, scale, ids, w, stream=None):
+    T, E = logits.shape
+    k = ids.shape[1]
+    _ok(lib.mhc_moe_router_fwd(
+        *_act_ptr(logits, "logits"), T, E, k, score, bool(renorm), scale,
+        _ptr(ids, _I32, (T, k), "ids"), _ptr(w, _F32, (T, k), "w"), _stream(stream)))
+
+
+def mhc_moe_router_bwd(dw, logits, ids, score, renorm, scale, dlogits, stream=None):
+    T, E = logits.shape
+    k = ids.shape[1]
+    _ok(lib.mhc_moe_router_bwd(
+        _ptr(dw, _F32, (T, k), "dw"), *_act_ptr(logits, "logits"),
+        _ptr(ids, _I32, (T, k), "ids"), T, E, k, score, bool(renorm), scale,
+        _ptr(dlogits, logits.dtype, (T, E), "dlogits"), _stream(stream)))
+
+
+def mhc_moe_rows(T: int, k: int, E: int, align: int) -> int:
+    """Rows to allocate for the sorted slots of T tokens with k experts each."""
+    return int(lib.mhc_moe_rows(T, k, E, align))
+
+
+def mhc_moe_sort(ids, align, counts, offsets, row_of, slot_of, stream=None):
+    T, k = ids.shape
+    E, R = counts.shape[0], slot_of.shape[0]
+    _ok(lib.mhc_moe_sort(
+        _ptr(ids, _I32, name="ids"), T, k, E, align, R, _ptr(counts, _I32, (E,), "counts"),
+        _ptr(offsets, _I32, (E + 1,), "offsets"), _ptr(row_of, _I32, (T, k), "row_of"),
+        _ptr(slot_of, _I32, (R,), "slot_of"), _stream(stream)))
+
+
+def mhc_moe_dispatch_fwd(x, row_of, slot_of, xs, stream=None):
+    T, C = x.shape
+    k, R = row_of.shape[1], xs.shape[0]
+    _ok(lib.mhc_moe_dispatch_fwd(
+        *_act_ptr(x, "x"), _ptr(row_of, _I32, (T, k), "row_of"),
+        _ptr(slot_of, _I32, (R,), "slot_of"), T, k, R, C, _ptr(xs, x.dtype, (R, C), "xs"),
+        _stream(stream)))
+
+
+def mhc_moe_dispatch_bwd(dxs, row_of, dx, stream=None):
+    R, C = dxs.shape
+    T, k = row_of.shape
+    _ok(lib.mhc_moe_dispatch_bwd(
+        *_act_ptr(dxs, "dxs"), _ptr(row_of, _I32, name="row_of"), T, k, R, C,
+        _ptr(dx, dxs.dtype, (T, C), "dx"), _stream(stream)))
+
+
+def mhc_moe_combine_fwd(ys, w, row_of, f, stream=None):
+    R, C = ys.shape
+    T, k = row_of.shape
+    _ok(lib.mhc_moe_combine_fwd(
+        *_act_ptr(ys, "ys"), _ptr(w, _F32, (T, k), "w"),
+        _ptr(row_of, _I32, name="row_of"), T, k, R, C, _ptr(f, ys.dtype, (T, C), "f"),
+        _stream(stream)))
+
+
+def mhc_moe_combine_bwd(df, ys, w, row_of, slot_of, dys, dw=None, stream=None):
+    code = _act(dys, "dys")
+    R, C = dys.shape
+    T, k = row_of.shape
+    _ok(lib.mhc_moe_combine_bwd(
+        _ptr(df, dys.dtype, (T, C), "df"), _ptr(ys, dys.dtype, (R, C), "ys"), code,
+        _ptr(w, _F32, (T, k), "w"), _ptr(row_of, _I32, name="row_of"),
+        _ptr(slot_of, _I32, (R,), "slot_of"), T, k, R, C, _ptr(dys, name="dys"),
+        _ptr(dw, _F32, (T, k), "dw"), _stream(stream)))
 
 
 def mhc_set_batch_invariant(on: bool) -> None:

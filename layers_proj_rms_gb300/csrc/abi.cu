@@ -9,6 +9,8 @@
 
 #include "../../include/mhc.h"
 #include "launch.h"
+#include "moe.h"
+#include "qk.h"
 
 using mhc::bf16;
 
@@ -116,6 +118,20 @@ struct Check {
     {
         if (st == MHC_OK && !(e >= 0.f && isfinite(e)))
             st = fail(MHC_ERR_BAD_ARG, "%s: %s = %g must be finite and >= 0", fn, name, double(e));
+        return *this;
+    }
+    Check &dtype(int d)
+    {
+        if (st == MHC_OK && (d < MHC_BF16 || d > MHC_FP32))
+            st = fail(MHC_ERR_BAD_ARG, "%s: dtype = %d is none of MHC_BF16, MHC_FP16, MHC_FP32", fn,
+                      d);
+        return *this;
+    }
+    Check &range(int64_t v, int64_t lo, int64_t hi, const char *name)
+    {
+        if (st == MHC_OK && (v < lo || v > hi))
+            st = fail(MHC_ERR_BAD_SHAPE, "%s: %s = %lld outside [%lld, %lld]", fn, name,
+                      (long long)v, (long long)lo, (long long)hi);
         return *this;
     }
     Check &ws(const void *p, size_t have, size_t need)
@@ -251,11 +267,14 @@ mhc_status mhc_device_error(int *code, mhc_stream_t stream)
 
 size_t mhc_workspace_bytes(mhc_op op, int64_t T, int n, int64_t C)
 {
+    if (op == MHC_OP_QK_NORM_ROPE_BWD)  // n = Hq + Hk, C = D
+        return T < 0 || n < 0 || C < 1 || C > MHC_MAX_HEAD_DIM ? 0 : mhc::qk_bwd_ws_bytes(T, n, C);
     if (T < 0 || C < 8 || C % 8 != 0) return 0;
     if (op == MHC_OP_RMSNORM_RESIDUAL_BWD) return mhc::norm_ws_bytes(T, C);  // n unused
     if (n != 4 && n != 8) return 0;
     switch (op) {
     case MHC_OP_RMSNORM_RESIDUAL_BWD: return 0;
+    case MHC_OP_QK_NORM_ROPE_BWD: return 0;
     case MHC_OP_H_AGGREGATE_RMSNORM_BWD: return mhc::norm_ws_bytes(T, C);
     case MHC_OP_H_AGGREGATE_STATIC_BWD: return mhc::agg_static_ws_bytes(T, n);
     case MHC_OP_PROJ_RMS_PARTIAL_FWD: return mhc::proj_fwd_ws_bytes(T, n, C);
@@ -821,6 +840,275 @@ mhc_status mhc_proj_rms_partial_bwd(const mhc_bf16 *x_shard, const float *W_shar
                                reinterpret_cast<const bf16 *>(x_shard), W_shard, du, coef, T, n, Cs,
                                reinterpret_cast<bf16 *>(dx_shard), dW_shard, ws, fault_ptr(),
                                stream));
+}
+
+// ---------------------------------------------------------------------------
+// the entry of attention: q/k norm and rotation
+// ---------------------------------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+// Fills one of q, k; strides: (token, head) pairs of the tensors in `order`.
+// A tensor of which only one token or head exists has no stride to check.
+void qk_tensor(Check &ck, mhc::QkTensor &m, const char *name, int64_t T, int H, int D, int es,
+               const void *x, const int64_t *xs, const void *up, const int64_t *us, void *out,
+               const int64_t *os, const float *gamma, float *dgamma)
+{
+    const int64_t plain[2] = {int64_t(H) * D, D};
+    xs = xs ? xs : plain;
+    us = us ? us : plain;
+    os = os ? os : plain;
+    m = {x, up, out, xs[0], xs[1], us[0], us[1], os[0], os[1], gamma, dgamma, H};
+    if (ck.st || H == 0) return;
+    auto bad = [&](mhc_status st, const char *what) {
+        if (ck.st == MHC_OK) ck.st = fail(st, "%s: %s: %s", ck.fn, name, what);
+    };
+    if (!x || !out) bad(MHC_ERR_NULL_PTR, "a tensor is NULL");
+    for (const void *p : {x, up, static_cast<const void *>(out)})
+        if (reinterpret_cast<uintptr_t>(p) % es) bad(MHC_ERR_MISALIGNED, "a tensor is off its elements");
+    for (const int64_t *st : {xs, us, os})
+        for (int i = 0; i < 2; ++i)
+            if (st[i] < 0 || st[i] > (int64_t(1) << 60) / ((i ? H : T) > 0 ? (i ? H : T) : 1))
+                bad(MHC_ERR_BAD_SHAPE, "a stride is negative or too large");
+    if (ck.st) return;
+    // the output's heads must not overlap: token-major or head-major
+    const bool one_t = T <= 1, one_h = H <= 1;
+    const bool tok = (one_h || os[1] >= D) && (one_t || os[0] >= (H - 1) * (one_h ? 0 : os[1]) + D);
+    const bool head = (one_t || os[0] >= D) && (one_h || os[1] >= (T - 1) * (one_t ? 0 : os[0]) + D);
+    if (!tok && !head) bad(MHC_ERR_BAD_SHAPE, "the output's heads overlap");
+    const bool same = (one_t || xs[0] == os[0]) && (one_h || xs[1] == os[1]);
+    const bool same_up = (one_t || us[0] == os[0]) && (one_h || us[1] == os[1]);
+    if ((out == x && !same) || (out == up && !same_up))
+        bad(MHC_ERR_BAD_SHAPE, "a call in place needs the same strides");
+    if (one_t) m.x_t = m.up_t = m.out_t = 0;  // never used
+    if (one_h) m.x_h = m.up_h = m.out_h = 0;
+}
+
+void qk_common(Check &ck, mhc::QkArgs &a, int dtype, const float *cs, const float *sn,
+               const int32_t *pos, int64_t T, int Hq, int Hk, int D, int R, int64_t P,
+               int interleaved, float eps)
+{
+    ck.dtype(dtype).count(T, "T").range(Hq, 0, 1 << 16, "Hq").range(Hk, 0, 1 << 16, "Hk");
+    ck.range(D, 1, MHC_MAX_HEAD_DIM, "D").range(R, 0, D, "R").count(P, "P").eps(eps, "eps");
+    ck.fits(T, int64_t(Hq + Hk) * D, "T*(Hq+Hk)*D").fits(P, R > 0 ? R : 1, "P*R");
+    if (ck.st == MHC_OK && R % 2) ck.st = fail(MHC_ERR_BAD_SHAPE, "%s: R = %d is odd", ck.fn, R);
+    if (ck.st == MHC_OK && R > 0 && T > 0 && !pos && T > P)
+        ck.st = fail(MHC_ERR_BAD_SHAPE, "%s: T = %lld positions, and %lld rows of cos, sin", ck.fn,
+                     (long long)T, (long long)P);
+    if (R > 0 && T > 0) ck.ptr(cs, "cos").ptr(sn, "sin");
+    if (ck.st == MHC_OK && reinterpret_cast<uintptr_t>(pos) % 4)
+        ck.st = fail(MHC_ERR_MISALIGNED, "%s: pos is not 4-byte aligned", ck.fn);
+    a.cs = cs;
+    a.sn = sn;
+    a.pos = pos;
+    a.T = T;
+    a.P = P;
+    a.D = D;
+    a.R = R;
+    a.interleaved = interleaved != 0;
+    a.eps = eps;
+}
+
+}  // namespace
+
+extern "C" {
+
+mhc_status mhc_qk_norm_rope_fwd(const void *q, const void *k, mhc_dtype dtype,
+                                const int64_t *strides, const float *gamma_q,
+                                const float *gamma_k, const float *cos, const float *sin,
+                                const int32_t *pos, int64_t T, int Hq, int Hk, int D, int R,
+                                int64_t P, int interleaved, float eps, void *q_out, void *k_out,
+                                mhc_stream_t stream)
+{
+    Check ck("mhc_qk_norm_rope_fwd");
+    mhc::QkArgs a = {};
+    qk_common(ck, a, int(dtype), cos, sin, pos, T, Hq, Hk, D, R, P, interleaved, eps);
+    ck.opt(gamma_q, "gamma_q").opt(gamma_k, "gamma_k");
+    if (ck.st || T == 0 || Hq + Hk == 0) return ck.st;
+    const int es = dtype == MHC_FP32 ? 4 : 2;
+    const int64_t *st = strides;
+    qk_tensor(ck, a.m[0], "q", T, Hq, D, es, q, st, nullptr, nullptr, q_out, st ? st + 4 : st,
+              gamma_q, nullptr);
+    qk_tensor(ck, a.m[1], "k", T, Hk, D, es, k, st ? st + 2 : st, nullptr, nullptr, k_out,
+              st ? st + 6 : st, gamma_k, nullptr);
+    if (ck.device().st) return ck.st;
+    a.fault = fault_ptr();
+    return launched(ck.fn, mhc::launch_qk_fwd(a, int(dtype), stream));
+}
+
+mhc_status mhc_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const void *q,
+                                const void *k, mhc_dtype dtype, const int64_t *strides,
+                                const float *gamma_q, const float *gamma_k, const float *cos,
+                                const float *sin, const int32_t *pos, int64_t T, int Hq, int Hk,
+                                int D, int R, int64_t P, int interleaved, float eps, void *dq,
+                                void *dk, float *dgamma_q, float *dgamma_k, void *ws,
+                                size_t ws_bytes, mhc_stream_t stream)
+{
+    Check ck("mhc_qk_norm_rope_bwd");
+    mhc::QkArgs a = {};
+    qk_common(ck, a, int(dtype), cos, sin, pos, T, Hq, Hk, D, R, P, interleaved, eps);
+    ck.opt(gamma_q, "gamma_q").opt(gamma_k, "gamma_k");
+    ck.opt(dgamma_q, "dgamma_q").opt(dgamma_k, "dgamma_k");
+    if (ck.st) return ck.st;
+    if (T == 0 || Hq + Hk == 0) {  // the sums over no heads are zero
+        if ((!dgamma_q && !dgamma_k) || ck.device().st) return ck.st;
+        cudaError_t e = cudaSuccess;
+        for (float *g : {dgamma_q, dgamma_k})
+            if (g && e == cudaSuccess) e = cudaMemsetAsync(g, 0, size_t(D) * sizeof(float), stream);
+        return launched(ck.fn, e);
+    }
+    const int es = dtype == MHC_FP32 ? 4 : 2;
+    const int64_t *st = strides;
+    auto at = [&](int i) { return st ? st + i : st; };
+    if ((Hq && !dq_out) || (Hk && !dk_out))
+        return fail(MHC_ERR_NULL_PTR, "%s: an upstream gradient is NULL", ck.fn);
+    qk_tensor(ck, a.m[0], "q", T, Hq, D, es, q, at(4), dq_out, at(0), dq, at(8), gamma_q, dgamma_q);
+    qk_tensor(ck, a.m[1], "k", T, Hk, D, es, k, at(6), dk_out, at(2), dk, at(10), gamma_k, dgamma_k);
+    if (dgamma_q || dgamma_k) ck.ws(ws, ws_bytes, mhc::qk_bwd_ws_bytes(T, Hq + Hk, D));
+    if (ck.device().st) return ck.st;
+    a.fault = fault_ptr();
+    return launched(ck.fn, mhc::launch_qk_bwd(a, int(dtype), static_cast<float *>(ws), stream));
+}
+
+// ---------------------------------------------------------------------------
+// mixture of experts: router, sort, dispatch, combine
+// ---------------------------------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+void moe_router_args(Check &ck, int64_t T, int E, int k, int dtype, int score, float scale)
+{
+    ck.dtype(dtype).count(T, "T").range(E, 1, MHC_MOE_MAX_EXPERTS, "E");
+    ck.range(k, 1, E < MHC_MOE_MAX_K ? E : MHC_MOE_MAX_K, "k").range(T, 0, INT32_MAX, "T");
+    if (ck.st == MHC_OK && score != MHC_SCORE_SOFTMAX && score != MHC_SCORE_SIGMOID)
+        ck.st = fail(MHC_ERR_BAD_ARG, "%s: score = %d is neither softmax nor sigmoid", ck.fn, score);
+    if (ck.st == MHC_OK && !isfinite(scale))
+        ck.st = fail(MHC_ERR_BAD_ARG, "%s: scale = %g must be finite", ck.fn, double(scale));
+}
+
+// T tokens of k slots, R sorted rows of C channels
+void moe_rows_args(Check &ck, int64_t T, int k, int64_t R, int64_t C, int dtype)
+{
+    ck.dtype(dtype).range(T, 0, INT32_MAX, "T").range(k, 1, MHC_MOE_MAX_K, "k");
+    ck.range(T * (ck.st ? 0 : k), 0, INT32_MAX, "T*k").range(R, 0, INT32_MAX, "R").channels(C);
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t mhc_moe_rows(int64_t T, int k, int E, int align)
+{
+    if (T < 0 || T > INT32_MAX || k < 1 || k > MHC_MOE_MAX_K || E < 1 || E > MHC_MOE_MAX_EXPERTS ||
+        align < 1 || align > MHC_MOE_MAX_ALIGN)
+        return -1;
+    return mhc::moe_rows(T, k, E, align);
+}
+
+mhc_status mhc_moe_router_fwd(const void *logits, mhc_dtype dtype, int64_t T, int E, int k,
+                              mhc_score score, int renorm, float scale, int32_t *ids, float *w,
+                              mhc_stream_t stream)
+{
+    Check ck("mhc_moe_router_fwd");
+    moe_router_args(ck, T, E, k, int(dtype), int(score), scale);
+    if (ck.st || T == 0) return ck.st;
+    ck.ptr(logits, "logits").ptr(ids, "ids").ptr(w, "w").device();
+    if (ck.st) return ck.st;
+    return launched(ck.fn, mhc::launch_moe_router_fwd(logits, int(dtype), T, E, k, int(score),
+                                                      renorm != 0, scale, ids, w, stream));
+}
+
+mhc_status mhc_moe_router_bwd(const float *dw, const void *logits, mhc_dtype dtype,
+                              const int32_t *ids, int64_t T, int E, int k, mhc_score score,
+                              int renorm, float scale, void *dlogits, mhc_stream_t stream)
+{
+    Check ck("mhc_moe_router_bwd");
+    moe_router_args(ck, T, E, k, int(dtype), int(score), scale);
+    if (ck.st || T == 0) return ck.st;
+    ck.ptr(dw, "dw").ptr(logits, "logits").ptr(ids, "ids").ptr(dlogits, "dlogits").device();
+    if (ck.st) return ck.st;
+    return launched(ck.fn,
+                    mhc::launch_moe_router_bwd(dw, logits, int(dtype), ids, T, E, k, int(score),
+                                               renorm != 0, scale, dlogits, fault_ptr(), stream));
+}
+
+mhc_status mhc_moe_sort(const int32_t *ids, int64_t T, int k, int E, int align, int64_t R,
+                        int32_t *counts, int32_t *offsets, int32_t *row_of, int32_t *slot_of,
+                        mhc_stream_t stream)
+{
+    Check ck("mhc_moe_sort");
+    ck.range(T, 0, INT32_MAX, "T").range(k, 1, MHC_MOE_MAX_K, "k");
+    ck.range(E, 1, MHC_MOE_MAX_EXPERTS, "E").range(align, 1, MHC_MOE_MAX_ALIGN, "align");
+    if (ck.st) return ck.st;
+    ck.range(T * k, 0, INT32_MAX, "T*k").range(R, mhc::moe_rows(T, k, E, align), INT32_MAX, "R");
+    ck.ptr(counts, "counts").ptr(offsets, "offsets");
+    if (T > 0) ck.ptr(ids, "ids").ptr(row_of, "row_of");
+    if (R > 0) ck.ptr(slot_of, "slot_of");
+    if (ck.device().st) return ck.st;
+    return launched(ck.fn, mhc::launch_moe_sort(ids, T * k, E, align, R, counts, offsets, row_of,
+                                                slot_of, fault_ptr(), stream));
+}
+
+mhc_status mhc_moe_dispatch_fwd(const void *x, mhc_dtype dtype, const int32_t *row_of,
+                                const int32_t *slot_of, int64_t T, int k, int64_t R, int64_t C,
+                                void *xs, mhc_stream_t stream)
+{
+    Check ck("mhc_moe_dispatch_fwd");
+    moe_rows_args(ck, T, k, R, C, int(dtype));
+    if (ck.st || R == 0) return ck.st;
+    if (T > 0) ck.ptr(x, "x").ptr(row_of, "row_of");
+    ck.ptr(slot_of, "slot_of").ptr(xs, "xs").device();
+    if (ck.st) return ck.st;
+    return launched(ck.fn, mhc::launch_moe_dispatch_fwd(x, int(dtype), row_of, slot_of, T, k, R, C,
+                                                        xs, fault_ptr(), stream));
+}
+
+mhc_status mhc_moe_dispatch_bwd(const void *dxs, mhc_dtype dtype, const int32_t *row_of,
+                                int64_t T, int k, int64_t R, int64_t C, void *dx,
+                                mhc_stream_t stream)
+{
+    Check ck("mhc_moe_dispatch_bwd");
+    moe_rows_args(ck, T, k, R, C, int(dtype));
+    if (ck.st || T == 0) return ck.st;
+    if (R > 0) ck.ptr(dxs, "dxs");
+    ck.ptr(row_of, "row_of").ptr(dx, "dx").device();
+    if (ck.st) return ck.st;
+    return launched(ck.fn, mhc::launch_moe_combine_fwd(dxs, int(dtype), nullptr, row_of, T, k, R, C,
+                                                       dx, fault_ptr(), stream));
+}
+
+mhc_status mhc_moe_combine_fwd(const void *ys, mhc_dtype dtype, const float *w,
+                               const int32_t *row_of, int64_t T, int k, int64_t R, int64_t C,
+                               void *f, mhc_stream_t stream)
+{
+    Check ck("mhc_moe_combine_fwd");
+    moe_rows_args(ck, T, k, R, C, int(dtype));
+    if (ck.st || T == 0) return ck.st;
+    if (R > 0) ck.ptr(ys, "ys");
+    ck.opt(w, "w").ptr(row_of, "row_of").ptr(f, "f").device();
+    if (ck.st) return ck.st;
+    return launched(ck.fn, mhc::launch_moe_combine_fwd(ys, int(dtype), w, row_of, T, k, R, C, f,
+                                                       fault_ptr(), stream));
+}
+
+mhc_status mhc_moe_combine_bwd(const void *df, const void *ys, mhc_dtype dtype, const float *w,
+                               const int32_t *row_of, const int32_t *slot_of, int64_t T, int k,
+                               int64_t R, int64_t C, void *dys, float *dw, mhc_stream_t stream)
+{
+    Check ck("mhc_moe_combine_bwd");
+    moe_rows_args(ck, T, k, R, C, int(dtype));
+    if (ck.st || (T == 0 && R == 0)) return ck.st;
+    if (T > 0) ck.ptr(df, "df").ptr(row_of, "row_of");
+    if (R > 0) ck.ptr(slot_of, "slot_of").ptr(dys, "dys");
+    if (R > 0 && dw) ck.ptr(ys, "ys");
+    ck.opt(w, "w").opt(dw, "dw").device();
+    if (ck.st) return ck.st;
+    return launched(ck.fn, mhc::launch_moe_combine_bwd(df, ys, int(dtype), w, row_of, slot_of, T, k,
+                                                       R, C, dys, dw, fault_ptr(), stream));
 }
 
 }  // extern "C"

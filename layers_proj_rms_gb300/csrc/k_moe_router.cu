@@ -1,0 +1,261 @@
+// Top-k router: ids [T, k] of the k largest logits of each token (ties to the
+// lowest index, NaN above everything) and their weights, and the gradient.
+//
+//   softmax:          w_j = scale p_j, p = softmax over all E logits
+//   softmax, renorm:  w_j = scale softmax over the k chosen logits
+//   sigmoid:          w_j = scale s(l_j), s the logistic function
+//   sigmoid, renorm:  w_j = scale s_j / sum of the chosen s, formed as the
+//                     softmax of log s over the chosen (no underflow)
+//   a row whose chosen (softmax: whose all) logits are -inf has weights 0.
+//   backward, a_j = scale dw_j:
+//     softmax:          dl_e = p_e (sum_{j: id_j = e} a_j - sum_j a_j p_j)
+//     softmax, renorm:  dl_j = v_j (a_j - sum_i a_i v_i), v = w / scale
+//     sigmoid:          dl_j = a_j s_j (1 - s_j)
+//     sigmoid, renorm:  dl_j = v_j (1 - s_j) (a_j - sum_i a_i v_i)
+//   dlogits of the experts not chosen are 0 but for the plain softmax.
+//
+// One warp per token; lane l holds logits l, l + 32, ...  The choice compares
+// logits as stored (monotone integer keys), never computed scores, so it is
+// exact.  Chosen slot j lives in lane j (k <= 32).
+#include "elem.cuh"
+#include "launch.h"
+#include "moe.h"
+
+namespace mhc {
+
+constexpr int kFaultChoice = 204;  // backward: an id outside [-1, E)
+
+namespace {
+
+constexpr int kRouterWarps = 4;
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, m));
+    return v;
+}
+
+__device__ __forceinline__ float widen1(bf16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float widen1(fp16 v) { return __half2float(v); }
+__device__ __forceinline__ float widen1(float v) { return v; }
+__device__ __forceinline__ void narrow1(float f, bf16 &o) { o = __float2bfloat16_rn(f); }
+__device__ __forceinline__ void narrow1(float f, fp16 &o) { o = __float2half_rn(f); }
+__device__ __forceinline__ void narrow1(float f, float &o) { o = f; }
+
+// Ascending integer key of a float; > 0; equal for -0 and 0; NaN the largest.
+__device__ __forceinline__ unsigned key_of(float f)
+{
+    if (f != f) return 0xffffffffu;
+    const unsigned u = __float_as_uint(f + 0.f);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ float logistic(float l) { return 1.f / (1.f + expf(-l)); }
+__device__ __forceinline__ float log_logistic(float l)
+{
+    return fminf(l, 0.f) - log1pf(expf(-fabsf(l)));
+}
+
+// Softmax of one value per lane over the lanes that are `on`; -inf everywhere
+// (or no lane on) gives 0.
+__device__ __forceinline__ float lane_softmax(float v, bool on)
+{
+    const float m = warp_max(on ? v : -INFINITY);  // a NaN is passed over here, not below
+    const float p = on && (m != -INFINITY || v != v) ? expf(v - m) : 0.f;
+    const float s = warp_sum(p);
+    return s == 0.f ? 0.f : p / s;
+}
+
+template <class T, int NV>
+__device__ __forceinline__ void load_row(const T *row, int E, int lane, float (&l)[NV])
+{
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        l[i] = e < E ? widen1(row[e]) : -INFINITY;
+    }
+}
+
+// max and sum of exp(l - max) over the row
+template <int NV>
+__device__ __forceinline__ void row_stats(const float (&l)[NV], float &m, float &sum)
+{
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+    sum = 0.f;
+    if (m == -INFINITY) m = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) sum += expf(l[i] - m);
+    sum = warp_sum(sum);
+}
+
+template <class T, int NV>
+__global__ void __launch_bounds__(kRouterWarps * 32)
+    k_moe_router(const T *__restrict__ logits, int64_t tokens, int E, int k, int score,
+                 int renorm, float scale, int32_t *__restrict__ ids, float *__restrict__ w)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = int64_t(blockIdx.x) * kRouterWarps + (threadIdx.x >> 5);
+    if (t >= tokens) return;
+    float l[NV];
+    load_row<T, NV>(logits + t * E, E, lane, l);
+    unsigned key[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) key[i] = lane + 32 * i < E ? key_of(l[i]) : 0u;
+    int my_id = 0;
+    float my_l = -INFINITY;
+    for (int j = 0; j < k; ++j) {
+        unsigned best = 0u;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                at = i;
+            }
+        const unsigned top = __reduce_max_sync(kFull, best);
+        const int e = int(__reduce_min_sync(kFull, best == top ? unsigned(lane + 32 * at) : ~0u));
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (e == lane + 32 * i) {
+                key[i] = 0u;
+                v = l[i];
+            }
+        v = __shfl_sync(kFull, v, e & 31);
+        if (lane == j) {
+            my_id = e;
+            my_l = v;
+        }
+    }
+    const bool on = lane < k;
+    float p;
+    if (renorm) {
+        p = lane_softmax(score == 0 ? my_l : log_logistic(my_l), on);
+    } else if (score == 0) {
+        float m, sum;
+        row_stats<NV>(l, m, sum);
+        p = sum == 0.f ? 0.f : expf(my_l - m) / sum;
+    } else {
+        p = logistic(my_l);
+    }
+    if (on) {
+        ids[t * k + lane] = my_id;
+        w[t * k + lane] = scale * p;
+    }
+}
+
+template <class T, int NV>
+__global__ void __launch_bounds__(kRouterWarps * 32)
+    k_moe_router_bwd(const float *__restrict__ dw, const T *__restrict__ logits,
+                     const int32_t *__restrict__ ids, int64_t tokens, int E, int k, int score,
+                     int renorm, float scale, T *__restrict__ dlogits, int *fault)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = int64_t(blockIdx.x) * kRouterWarps + (threadIdx.x >> 5);
+    if (t >= tokens) return;
+    const T *row = logits + t * E;
+    int id = lane < k ? __ldg(ids + t * k + lane) : -1;
+    if (id < -1 || id >= E) {
+        report_fault(fault, kFaultChoice);
+        id = -1;
+    }
+    const bool on = id >= 0;
+    const float a = on ? scale * __ldg(dw + t * k + lane) : 0.f;
+    const float lj = on ? widen1(row[id]) : -INFINITY;
+    float d;         // this lane's slot's gradient
+    float out[NV];   // dlogits of experts lane, lane + 32, ...
+#pragma unroll
+    for (int i = 0; i < NV; ++i) out[i] = 0.f;
+    if (renorm) {
+        const float v = lane_softmax(score == 0 ? lj : log_logistic(lj), on);
+        d = v * (a - warp_sum(a * v));
+        if (score != 0) d *= logistic(-lj);
+    } else if (score == 0) {
+        float l[NV], m, sum;
+        load_row<T, NV>(row, E, lane, l);
+        row_stats<NV>(l, m, sum);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const float v = on ? expf(lj - m) * inv : 0.f;
+        const float inner = warp_sum(a * v);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) out[i] = -(expf(l[i] - m) * inv * inner);
+        d = a * v;
+    } else {
+        const float v = logistic(lj);
+        d = a * v * logistic(-lj);
+    }
+    if (!on) d = 0.f;
+    for (int j = 0; j < k; ++j) {
+        const int e = __shfl_sync(kFull, id, j);
+        const float v = __shfl_sync(kFull, d, j);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (e == lane + 32 * i) out[i] += v;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        if (e < E) narrow1(out[i], dlogits[t * E + e]);
+    }
+}
+
+#define MHC_ROUTER_NV(NV_, ...)                          \
+    if (E <= 32) { constexpr int NV_ = 1; __VA_ARGS__; } \
+    else if (E <= 64) { constexpr int NV_ = 2; __VA_ARGS__; } \
+    else if (E <= 128) { constexpr int NV_ = 4; __VA_ARGS__; } \
+    else if (E <= 256) { constexpr int NV_ = 8; __VA_ARGS__; } \
+    else if (E <= 512) { constexpr int NV_ = 16; __VA_ARGS__; } \
+    else { constexpr int NV_ = 32; __VA_ARGS__; }
+
+template <class T>
+cudaError_t fwd_of(const void *logits, int64_t tokens, int E, int k, int score, int renorm,
+                   float scale, int32_t *ids, float *w, cudaStream_t s)
+{
+    const dim3 g(unsigned((tokens + kRouterWarps - 1) / kRouterWarps));
+    MHC_ROUTER_NV(NV, return launch_k(k_moe_router<T, NV>, g, dim3(kRouterWarps * 32), 0, s,
+                                      static_cast<const T *>(logits), tokens, E, k, score, renorm,
+                                      scale, ids, w));
+}
+
+template <class T>
+cudaError_t bwd_of(const float *dw, const void *logits, const int32_t *ids, int64_t tokens, int E,
+                   int k, int score, int renorm, float scale, void *dlogits, int *fault,
+                   cudaStream_t s)
+{
+    const dim3 g(unsigned((tokens + kRouterWarps - 1) / kRouterWarps));
+    MHC_ROUTER_NV(NV, return launch_k(k_moe_router_bwd<T, NV>, g, dim3(kRouterWarps * 32), 0, s,
+                                      dw, static_cast<const T *>(logits), ids, tokens, E, k, score,
+                                      renorm, scale, static_cast<T *>(dlogits), fault));
+}
+
+}  // namespace
+
+cudaError_t launch_moe_router_fwd(const void *logits, int dtype, int64_t T, int E, int k,
+                                  int score, int renorm, float scale, int32_t *ids, float *w,
+                                  cudaStream_t s)
+{
+    MHC_PROF("k_moe_router", s);
+    return dtype == 0   ? fwd_of<bf16>(logits, T, E, k, score, renorm, scale, ids, w, s)
+           : dtype == 1 ? fwd_of<fp16>(logits, T, E, k, score, renorm, scale, ids, w, s)
+                        : fwd_of<float>(logits, T, E, k, score, renorm, scale, ids, w, s);
+}
+
+cudaError_t launch_moe_router_bwd(const float *dw, const void *logits, int dtype,
+                                  const int32_t *ids, int64_t T, int E, int k, int score,
+                                  int renorm, float scale, void *dlogits, int *fault,
+                                  cudaStream_t s)
+{
+    MHC_PROF("k_moe_router_bwd", s);
+    return dtype == 0 ? bwd_of<bf16>(dw, logits, ids, T, E, k, score, renorm, scale, dlogits, fault, s)
+           : dtype == 1
+               ? bwd_of<fp16>(dw, logits, ids, T, E, k, score, renorm, scale, dlogits, fault, s)
+               : bwd_of<float>(dw, logits, ids, T, E, k, score, renorm, scale, dlogits, fault, s);
+}
+
+}  // namespace mhc

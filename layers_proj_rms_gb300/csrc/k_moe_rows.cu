@@ -1,0 +1,243 @@
+// Token rows to their experts' segments and back.
+//
+//   dispatch:      xs[r] = x[slot_of[r] / k], padding rows 0
+//   combine:       f[t] = sum_j w[t][j] ys[row_of[t][j]]     (w absent: 1; the
+//                  gradient of dispatch), dropped slots (-1) add nothing
+//   combine bwd:   dys[row] = w[t][j] df[t], padding rows 0;
+//                  dw[t][j] = sum_c df[t][c] ys[row][c], dropped slots 0
+//
+// All three are bound by HBM.  They walk over tokens, not over sorted rows: a
+// token's row is read once and its k rows are whole, contiguous 2C-byte rows
+// wherever they are, so every byte crosses HBM once.  Padding rows have no
+// token; each block clears those of its share of the sorted rows.
+// Sums over j are in ascending j and sums over c in an order fixed by C
+// alone, so a token's results do not depend on T or on its place.
+#include "elem.cuh"
+#include "launch.h"
+#include "moe.h"
+
+namespace mhc {
+
+constexpr int kFaultRow = 203;  // a row of the plan outside [-1, R)
+
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// The row of a slot: -1 if dropped, or if the plan is not one (a fault).
+__device__ __forceinline__ int64_t plan_row(const int32_t *row_of, int64_t slot, int64_t R,
+                                            int *fault)
+{
+    const int64_t r = __ldg(row_of + slot);
+    if (r >= -1 && r < R) return r;
+    report_fault(fault, kFaultRow);
+    return -1;
+}
+
+// Zeroes the padding rows among the block's share of the sorted rows.
+__device__ __forceinline__ void clear_padding(const int32_t *slot_of, int64_t R, int64_t chunks,
+                                              uint4 *out)
+{
+    const int64_t per = (R + gridDim.x - 1) / gridDim.x;
+    const int64_t r0 = per * blockIdx.x, r1 = r0 + per < R ? r0 + per : R;
+    for (int64_t r = r0; r < r1; ++r)
+        if (__ldg(slot_of + r) < 0)
+            for (int64_t q = threadIdx.x; q < chunks; q += blockDim.x)
+                st_stream(out + r * chunks + q, make_uint4(0, 0, 0, 0));
+}
+
+// chunks: 16-byte pieces of a row
+__global__ void __launch_bounds__(kRowThreads)
+    k_moe_dispatch(const uint4 *__restrict__ x, const int32_t *__restrict__ row_of,
+                   const int32_t *__restrict__ slot_of, int64_t T, int k, int64_t R,
+                   int64_t chunks, uint4 *__restrict__ xs, int *fault)
+{
+    pdl_wait();
+    for (int64_t t = blockIdx.x; t < T; t += gridDim.x)
+        for (int64_t q = threadIdx.x; q < chunks; q += blockDim.x) {
+            const uint4 v = ld_stream(x + t * chunks + q);
+            for (int j = 0; j < k; ++j) {
+                const int64_t r = plan_row(row_of, t * k + j, R, fault);
+                if (r >= 0) st_stream(xs + r * chunks + q, v);
+            }
+        }
+    clear_padding(slot_of, R, chunks, xs);
+}
+
+// One 8-element chunk of one token per thread.
+template <class T>
+__global__ void __launch_bounds__(kRowThreads)
+    k_moe_combine(const T *__restrict__ ys, const float *__restrict__ w,
+                  const int32_t *__restrict__ row_of, int64_t n, int k, int64_t R, int64_t C8,
+                  T *__restrict__ f, int *fault)
+{
+    pdl_wait();
+    const int64_t i = int64_t(blockIdx.x) * kRowThreads + threadIdx.x;
+    if (i >= n) return;
+    const int64_t t = i / C8, q = i - t * C8;
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        Vec<T, 8> v[8];
+        float wj[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            wj[j] = 0.f;
+            zero_vec(v[j]);
+            if (j0 + j < k) {
+                const int64_t slot = t * k + j0 + j, r = plan_row(row_of, slot, R, fault);
+                if (r >= 0) {
+                    wj[j] = w ? __ldg(w + slot) : 1.f;
+                    ld_vec(v[j], ys + (r * C8 + q) * 8);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float y[8];
+            widen(v[j], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(wj[j], y[e], acc[e]);
+        }
+    }
+    Vec<T, 8> o;
+    narrow(acc, o);
+    st_vec(f + i * 8, o);
+}
+
+// One token per block; the k sums of dw stay in registers over the row.
+template <class T>
+__global__ void __launch_bounds__(kRowThreads)
+    k_moe_combine_bwd(const T *__restrict__ df, const T *__restrict__ ys,
+                      const float *__restrict__ w, const int32_t *__restrict__ row_of,
+                      const int32_t *__restrict__ slot_of, int64_t T_, int k, int64_t R,
+                      int64_t C8, T *__restrict__ dys, float *__restrict__ dw, int *fault)
+{
+    __shared__ float red[8][kRowThreads / 32];
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int64_t t = blockIdx.x; t < T_; t += gridDim.x)
+        for (int j0 = 0; j0 < k; j0 += 8) {
+            int64_t row[8];
+            float wj[8], acc[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                acc[j] = wj[j] = 0.f;
+                row[j] = -1;
+                if (j0 + j < k) {
+                    const int64_t slot = t * k + j0 + j;
+                    row[j] = plan_row(row_of, slot, R, fault);
+                    if (row[j] >= 0) wj[j] = w ? __ldg(w + slot) : 1.f;
+                }
+            }
+            for (int64_t q = threadIdx.x; q < C8; q += blockDim.x) {
+                Vec<T, 8> dv, yv[8];
+                ld_vec(dv, df + (t * C8 + q) * 8);
+                if (dw)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (row[j] >= 0) ld_vec(yv[j], ys + (row[j] * C8 + q) * 8);
+                float d[8];
+                widen(dv, d);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (row[j] >= 0) {
+                        float o[8];
+                        if (dw) {
+                            float y[8];
+                            widen(yv[j], y);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) acc[j] = fmaf(d[e], y[e], acc[j]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = wj[j] * d[e];
+                        Vec<T, 8> ov;
+                        narrow(o, ov);
+                        st_vec(dys + (row[j] * C8 + q) * 8, ov);
+                    }
+            }
+            if (!dw) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float s = warp_sum(acc[j]);
+                if (lane == 0) red[j][warp] = s;
+            }
+            __syncthreads();
+            if (threadIdx.x < 8 && j0 + int(threadIdx.x) < k) {
+                float s = 0.f;
+                for (int i = 0; i < int(blockDim.x >> 5); ++i) s += red[threadIdx.x][i];
+                dw[t * k + j0 + threadIdx.x] = s;
+            }
+            __syncthreads();
+        }
+    clear_padding(slot_of, R, C8 * int64_t(sizeof(T)) / 2, reinterpret_cast<uint4 *>(dys));
+}
+
+// A block per token, and no more than eight sorted rows to look over for each.
+unsigned row_blocks(int64_t T, int64_t R)
+{
+    const int64_t n = T > (R + 7) / 8 ? T : (R + 7) / 8, cap = int64_t(kSplitSms) * 64;
+    return unsigned(n < cap ? n : cap);
+}
+
+int row_threads(int64_t chunks)
+{
+    const int64_t t = (chunks + 31) / 32 * 32;
+    return int(t < kRowThreads ? t : kRowThreads);
+}
+
+template <class T>
+cudaError_t combine_of(const void *ys, const float *w, const int32_t *row_of, int64_t tokens,
+                       int k, int64_t R, int64_t C, void *f, int *fault, cudaStream_t s)
+{
+    const int64_t n = tokens * (C / 8), blocks = (n + kRowThreads - 1) / kRowThreads;
+    MHC_PROF("k_moe_combine", s);
+    return launch_k(k_moe_combine<T>, dim3(unsigned(blocks)), dim3(kRowThreads), 0, s,
+                    static_cast<const T *>(ys), w, row_of, n, k, R, C / 8, static_cast<T *>(f),
+                    fault);
+}
+
+template <class T>
+cudaError_t combine_bwd_of(const void *df, const void *ys, const float *w, const int32_t *row_of,
+                           const int32_t *slot_of, int64_t tokens, int k, int64_t R, int64_t C,
+                           void *dys, float *dw, int *fault, cudaStream_t s)
+{
+    MHC_PROF("k_moe_combine_bwd", s);
+    return launch_k(k_moe_combine_bwd<T>, dim3(row_blocks(tokens, R)), dim3(row_threads(C / 8)), 0,
+                    s, static_cast<const T *>(df), static_cast<const T *>(ys), w, row_of, slot_of,
+                    tokens, k, R, C / 8, static_cast<T *>(dys), dw, fault);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_dispatch_fwd(const void *x, int dtype, const int32_t *row_of,
+                                    const int32_t *slot_of, int64_t T, int k, int64_t R,
+                                    int64_t C, void *xs, int *fault, cudaStream_t s)
+{
+    const int64_t chunks = C * (dtype == 2 ? 4 : 2) / 16;
+    MHC_PROF("k_moe_dispatch", s);
+    return launch_k(k_moe_dispatch, dim3(row_blocks(T, R)), dim3(row_threads(chunks)), 0, s,
+                    static_cast<const uint4 *>(x), row_of, slot_of, T, k, R, chunks,
+                    static_cast<uint4 *>(xs), fault);
+}
+
+cudaError_t launch_moe_combine_fwd(const void *ys, int dtype, const float *w,
+                                   const int32_t *row_of, int64_t T, int k, int64_t R, int64_t C,
+                                   void *f, int *fault, cudaStream_t s)
+{
+    return dtype == 0   ? combine_of<bf16>(ys, w, row_of, T, k, R, C, f, fault, s)
+           : dtype == 1 ? combine_of<fp16>(ys, w, row_of, T, k, R, C, f, fault, s)
+                        : combine_of<float>(ys, w, row_of, T, k, R, C, f, fault, s);
+}
+
+cudaError_t launch_moe_combine_bwd(const void *df, const void *ys, int dtype, const float *w,
+                                   const int32_t *row_of, const int32_t *slot_of, int64_t T,
+                                   int k, int64_t R, int64_t C, void *dys, float *dw, int *fault,
+                                   cudaStream_t s)
+{
+    return dtype == 0 ? combine_bwd_of<bf16>(df, ys, w, row_of, slot_of, T, k, R, C, dys, dw, fault, s)
+           : dtype == 1
+               ? combine_bwd_of<fp16>(df, ys, w, row_of, slot_of, T, k, R, C, dys, dw, fault, s)
+               : combine_bwd_of<float>(df, ys, w, row_of, slot_of, T, k, R, C, dys, dw, fault, s);
+}
+
+}  // namespace mhc
