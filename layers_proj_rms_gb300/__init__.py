@@ -39,5 +39,6 @@ __all__ = [
 def __getattr__(name):
     if name in __all__:
         from . import _lib
-        return getattr(_lib, name)
+        value = globals()[name] = getattr(_lib, name)  # found without this function from now on
+        return value
     raise AttributeError(name)
