@@ -452,8 +452,11 @@ cudaError_t fwd_of(const QkArgs &a, cudaStream_t s)
     case 8:
         return qk_many(a) ? run_fwd<T, 8, 1, (sizeof(T) == 4 ? 2 : 4)>(a, s)
                           : run_fwd<T, 8, 1, 1>(a, s);
-    case 2: return run_fwd<T, 2, 4, 1>(a, s);
-    default: return run_fwd<T, 1, 8, 1>(a, s);
+    case 2:
+        if (a.D > 128) return run_fwd<T, 2, 4, 1>(a, s);
+        return qk_many(a) ? run_fwd<T, 2, 1, 4>(a, s) : run_fwd<T, 2, 1, 1>(a, s);
+    default:
+        return a.D > 128 ? run_fwd<T, 1, 8, 1>(a, s) : run_fwd<T, 1, 2, 2>(a, s);
     }
 }
 
@@ -464,8 +467,11 @@ cudaError_t bwd_of(const QkArgs &a, float *ws, cudaStream_t s)
     case 8:
         return qk_many(a) && sizeof(T) == 2 ? run_bwd<T, 8, 1, 2>(a, ws, s)
                                             : run_bwd<T, 8, 1, 1>(a, ws, s);
-    case 2: return run_bwd<T, 2, 4, 1>(a, ws, s);
-    default: return run_bwd<T, 1, 8, 1>(a, ws, s);
+    case 2:
+        if (a.D > 128) return run_bwd<T, 2, 4, 1>(a, ws, s);
+        return qk_many(a) ? run_bwd<T, 2, 1, 4>(a, ws, s) : run_bwd<T, 2, 1, 1>(a, ws, s);
+    default:
+        return a.D > 128 ? run_bwd<T, 1, 8, 1>(a, ws, s) : run_bwd<T, 1, 2, 2>(a, ws, s);
     }
 }
 
