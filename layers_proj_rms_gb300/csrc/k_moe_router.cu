@@ -16,7 +16,8 @@
 //
 // One warp per token; lane l holds logits l, l + 32, ...  The choice compares
 // logits as stored (monotone integer keys), never computed scores, so it is
-// exact.  Chosen slot j lives in lane j (k <= 32).
+// exact.  Chosen slot j lives in lane j (k <= 32).  What bounds it: the warp's
+// instructions (each round is one warp maximum and one step of a sorted list).
 #include "elem.cuh"
 #include "launch.h"
 #include "moe.h"
@@ -92,22 +93,49 @@ __device__ __forceinline__ void row_stats(const float (&l)[NV], float &m, float 
     sum = warp_sum(sum);
 }
 
-template <class T, int NV>
-__global__ void __launch_bounds__(kRouterWarps * 32)
-    k_moe_router(const T *__restrict__ logits, int64_t tokens, int E, int k, int score,
-                 int renorm, float scale, int32_t *__restrict__ ids, float *__restrict__ w)
+// Sorts NV (1, 2, 4, 8) registers in descending order: a merge network of
+// compare-exchanges (19 for eight values).
+template <int NV>
+__device__ __forceinline__ void sort_desc(unsigned (&p)[NV])
 {
-    pdl_wait();
+    auto cx = [&](int a, int b) {
+        const unsigned hi = max(p[a], p[b]), lo = min(p[a], p[b]);
+        p[a] = hi;
+        p[b] = lo;
+    };
+#pragma unroll
+    for (int w = 1; w < NV; w *= 2)           // merge sorted runs of w
+#pragma unroll
+        for (int d = w; d >= 1; d /= 2)
+#pragma unroll
+            for (int i = d % w; i + d < NV; i += 2 * d)
+#pragma unroll
+                for (int q = 0; q < d; ++q)
+                    if (i + q + d < NV && (i + q) / (2 * w) == (i + q + d) / (2 * w))
+                        cx(i + q, i + q + d);
+}
+
+// The choice packs a logit's key and its index into one word: the key's upper
+// upper 22 bits over 1023 - index, so that one integer maximum finds the
+// largest logit and, among equal ones, the lowest index.  22 bits hold the
+// whole of a bf16 or fp16 value (16 and 19 bits of its fp32 form).  Of a
+// 32-bit logit they do not: the order is then certain unless two neighbours of
+// the top k + 1 agree in them, and such a row (about 2 in 100 of normal logits
+// at E = 256, k = 8) is chosen again, by whole keys.
+__device__ __forceinline__ unsigned pack_of(float l, int e)
+{
+    return (key_of(l) & ~1023u) | unsigned(1023 - e);
+}
+
+// Exact choice by whole keys, one maximum at a time: lane j gets choice j.
+template <int NV>
+__device__ __noinline__ int choose_exact(const float (&l)[NV], int E, int k)
+{
     const int lane = threadIdx.x & 31;
-    const int64_t t = int64_t(blockIdx.x) * kRouterWarps + (threadIdx.x >> 5);
-    if (t >= tokens) return;
-    float l[NV];
-    load_row<T, NV>(logits + t * E, E, lane, l);
     unsigned key[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = lane + 32 * i < E ? key_of(l[i]) : 0u;
-    int my_id = 0;
-    float my_l = -INFINITY;
+    int mine = 0;
     for (int j = 0; j < k; ++j) {
         unsigned best = 0u;
         int at = 0;
@@ -119,33 +147,75 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
             }
         const unsigned top = __reduce_max_sync(kFull, best);
         const int e = int(__reduce_min_sync(kFull, best == top ? unsigned(lane + 32 * at) : ~0u));
-        float v = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (e == lane + 32 * i) {
-                key[i] = 0u;
-                v = l[i];
-            }
-        v = __shfl_sync(kFull, v, e & 31);
-        if (lane == j) {
-            my_id = e;
-            my_l = v;
-        }
+            if (e == lane + 32 * i) key[i] = 0u;
+        if (lane == j) mine = e;
     }
+    return mine;
+}
+
+template <class T, int NV>
+__global__ void __launch_bounds__(kRouterWarps * 32)
+    k_moe_router(const T *__restrict__ logits, int64_t tokens, int E, int k, int score,
+                 int renorm, float scale, int32_t *__restrict__ ids, float *__restrict__ w)
+{
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t t = int64_t(blockIdx.x) * kRouterWarps + (threadIdx.x >> 5);
+    if (t >= tokens) return;
+    const T *row = logits + t * E;
+    float l[NV];
+    load_row<T, NV>(row, E, lane, l);
+    unsigned p[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        p[i] = lane + 32 * i < E ? pack_of(l[i], lane + 32 * i) : 0u;
+    // up to eight values a lane are sorted, so that a round only looks at the
+    // head; more are searched in every round
+    constexpr bool kSorted = NV <= 8;
+    if constexpr (kSorted) sort_desc<NV>(p);
+    unsigned mine = 0u, last = 0u;
+    bool sure = true;
+    const int rounds = sizeof(T) == 2 || k == E ? k : k + 1;
+    for (int j = 0; j < rounds; ++j) {
+        unsigned best = p[0];
+        if constexpr (!kSorted)
+#pragma unroll
+            for (int i = 1; i < NV; ++i) best = max(best, p[i]);
+        const unsigned top = __reduce_max_sync(kFull, best);
+        if constexpr (kSorted) {
+            if (p[0] == top) {
+#pragma unroll
+                for (int i = 0; i + 1 < NV; ++i) p[i] = p[i + 1];
+                p[NV - 1] = 0u;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (p[i] == top) p[i] = 0u;
+        }
+        if (sizeof(T) == 4) sure = sure && (j == 0 || (top ^ last) >= 1024u);
+        last = top;
+        if (lane == j) mine = top;
+    }
+    int my_id = 1023 - int(mine & 1023u);
+    if (sizeof(T) == 4 && !sure) my_id = choose_exact<NV>(l, E, k);
     const bool on = lane < k;
-    float p;
+    const float my_l = on ? widen1(row[my_id]) : -INFINITY;
+    float v;
     if (renorm) {
-        p = lane_softmax(score == 0 ? my_l : log_logistic(my_l), on);
+        v = lane_softmax(score == 0 ? my_l : log_logistic(my_l), on);
     } else if (score == 0) {
         float m, sum;
         row_stats<NV>(l, m, sum);
-        p = sum == 0.f ? 0.f : expf(my_l - m) / sum;
+        v = sum == 0.f ? 0.f : expf(my_l - m) / sum;
     } else {
-        p = logistic(my_l);
+        v = logistic(my_l);
     }
     if (on) {
         ids[t * k + lane] = my_id;
-        w[t * k + lane] = scale * p;
+        w[t * k + lane] = scale * v;
     }
 }
 
