@@ -117,4 +117,67 @@ __device__ __forceinline__ void narrow(const float (&f)[V], Vec<T, V> &v)
     }
 }
 
+// V values for arithmetic: packed fp32 pairs (one instruction works on two
+// values), or a single fp32 where V = 1.
+__device__ __forceinline__ f32x2 e_mul(f32x2 a, f32x2 b) { return f2_mul(a, b); }
+__device__ __forceinline__ float e_mul(float a, float b) { return a * b; }
+__device__ __forceinline__ f32x2 e_fma(f32x2 a, f32x2 b, f32x2 c) { return f2_fma(a, b, c); }
+__device__ __forceinline__ float e_fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ void e_set(f32x2 &a, float v) { a = f2_make(v, v); }
+__device__ __forceinline__ void e_set(float &a, float v) { a = v; }
+__device__ __forceinline__ f32x2 e_neg(f32x2 a) { return a ^ 0x8000000080000000ull; }
+__device__ __forceinline__ float e_neg(float a) { return -a; }
+__device__ __forceinline__ float e_sum(f32x2 a)
+{
+    float lo, hi;
+    f2_split(a, lo, hi);
+    return lo + hi;
+}
+__device__ __forceinline__ float e_sum(float a) { return a; }
+// (lo, hi) -> (hi, lo)
+__device__ __forceinline__ f32x2 e_swap(f32x2 a)
+{
+    float lo, hi;
+    f2_split(a, lo, hi);
+    return f2_make(hi, lo);
+}
+__device__ __forceinline__ float e_swap(float a) { return a; }
+
+template <int V>
+struct Elems {
+    typedef f32x2 E;
+    static constexpr int N = V / 2;
+};
+template <>
+struct Elems<1> {
+    typedef float E;
+    static constexpr int N = 1;
+};
+
+template <class T, int V>
+__device__ __forceinline__ void widen_e(const Vec<T, V> &v, typename Elems<V>::E (&x)[Elems<V>::N])
+{
+    float f[V];
+    widen(v, f);
+    if constexpr (V == 1) {
+        x[0] = f[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) x[i] = f2_make(f[2 * i], f[2 * i + 1]);
+    }
+}
+
+template <class T, int V>
+__device__ __forceinline__ void narrow_e(const typename Elems<V>::E (&x)[Elems<V>::N], Vec<T, V> &v)
+{
+    float f[V];
+    if constexpr (V == 1) {
+        f[0] = x[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; ++i) f2_split(x[i], f[2 * i], f[2 * i + 1]);
+    }
+    narrow(f, v);
+}
+
 }  // namespace mhc

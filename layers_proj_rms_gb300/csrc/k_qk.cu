@@ -58,56 +58,92 @@ __device__ __forceinline__ void unit_at(int u, int hr, int half, bool inter, int
     }
 }
 
-// cos and sin of the V pairs of unit u.
-template <int V>
-__device__ __forceinline__ void load_rope(const float *cs, const float *sn, int64_t at,
-                                          float (&c)[V], float (&s)[V])
+// V consecutive fp32 values from p (global, read-only) or from shared memory.
+template <int V, bool SHARED>
+__device__ __forceinline__ void load_f(const float *p, float (&f)[V])
 {
     if constexpr (V == 8) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(cs + at) + q);
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(sn + at) + q);
-            c[4 * q] = cv.x; c[4 * q + 1] = cv.y; c[4 * q + 2] = cv.z; c[4 * q + 3] = cv.w;
-            s[4 * q] = sv.x; s[4 * q + 1] = sv.y; s[4 * q + 2] = sv.z; s[4 * q + 3] = sv.w;
+            const float4 *g = reinterpret_cast<const float4 *>(p) + q;
+            const float4 v = SHARED ? *g : __ldg(g);
+            f[4 * q] = v.x; f[4 * q + 1] = v.y; f[4 * q + 2] = v.z; f[4 * q + 3] = v.w;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            c[i] = __ldg(cs + at + i);
-            s[i] = __ldg(sn + at + i);
-        }
+        for (int i = 0; i < V; ++i) f[i] = SHARED ? p[i] : __ldg(p + i);
     }
 }
 
-// Rotates the V pairs of a unit by (c, s); sgn = -1 rotates back.
-template <int V>
-__device__ __forceinline__ void rotate(float (&a)[V], float (&b)[V], const float (&c)[V],
-                                       const float (&s)[V], bool inter, float sgn)
-{
-    auto turn = [&](float &u, float &v, float cc, float ss) {
-        const float x = u, y = v;
-        ss *= sgn;
-        u = x * cc - y * ss;
-        v = y * cc + x * ss;
-    };
-    if (V == 1 || !inter) {
+// What a unit's two chunks are multiplied by: cos for a chunk's own values and
+// sin for its partner's, with the signs of the forward rotation.  The partner
+// of chunk a is chunk b (half-split pairs), or each value's neighbour
+// (interleaved; INTER).
+template <int V, bool INTER>
+struct Rope {
+    typedef typename Elems<V>::E E;
+    static constexpr int N = Elems<V>::N, NR = INTER ? 2 * N : N;
+    E c[NR], s[NR];
+    __device__ __forceinline__ void load(const float *cs, const float *sn, int64_t at)
+    {
+        float fc[V], fs[V];
+        load_f<V, false>(cs + at, fc);
+        load_f<V, false>(sn + at, fs);
+        if constexpr (V == 1) {
+            c[0] = fc[0];
+            s[0] = fs[0];
+        } else if constexpr (INTER) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) turn(a[i], b[i], c[i], s[i]);
-    } else if constexpr (V > 1) {
+            for (int i = 0; i < V; ++i) {
+                c[i] = f2_make(fc[i], fc[i]);
+                s[i] = f2_make(-fs[i], fs[i]);
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-            turn(a[2 * i], a[2 * i + 1], c[i], s[i]);
-            turn(b[2 * i], b[2 * i + 1], c[V / 2 + i], s[V / 2 + i]);
+            for (int i = 0; i < N; ++i) {
+                c[i] = f2_make(fc[2 * i], fc[2 * i + 1]);
+                s[i] = f2_make(fs[2 * i], fs[2 * i + 1]);
+            }
         }
     }
-}
+    __device__ __forceinline__ E ca(int i) const { return c[i]; }
+    __device__ __forceinline__ E cb(int i) const { return INTER ? c[N + i] : c[i]; }
+    __device__ __forceinline__ E sa(int i) const { return INTER ? s[i] : e_neg(s[i]); }
+    __device__ __forceinline__ E sb(int i) const { return INTER ? s[N + i] : s[i]; }
+    // the value that stands beside a's (b's) element i
+    static __device__ __forceinline__ E pa(const E (&a)[N], const E (&b)[N], int i)
+    {
+        return INTER ? e_swap(a[i]) : b[i];
+    }
+    static __device__ __forceinline__ E pb(const E (&a)[N], const E (&b)[N], int i)
+    {
+        return INTER ? e_swap(b[i]) : a[i];
+    }
+};
 
-template <int V>
-__device__ __forceinline__ void load_gamma(const float *gamma, int at, bool on, float (&g)[V])
+// The block's copy of both gammas (1 where there is none), rows of Dp floats.
+__device__ __forceinline__ int gamma_row(int D) { return (D + 7) & ~7; }
+__device__ __forceinline__ void stage_gammas(const QkArgs &A, float *sg)
 {
+    const int Dp = gamma_row(A.D);
+    for (int i = threadIdx.x; i < 2 * Dp; i += blockDim.x) {
+        const int which = i >= Dp, d = which ? i - Dp : i;
+        const float *g = A.m[which].gamma;
+        sg[i] = g && d < A.D ? __ldg(g + d) : 1.f;
+    }
+    __syncthreads();
+}
+template <int V>
+__device__ __forceinline__ void gamma_e(const float *sg, typename Elems<V>::E (&g)[Elems<V>::N])
+{
+    float f[V];
+    load_f<V, true>(sg, f);
+    if constexpr (V == 1) {
+        g[0] = f[0];
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) g[i] = on ? (gamma ? __ldg(gamma + at + i) : 1.f) : 0.f;
+        for (int i = 0; i < V / 2; ++i) g[i] = f2_make(f[2 * i], f[2 * i + 1]);
+    }
 }
 
 // What a warp does: tensor, head set, first token.
@@ -135,29 +171,54 @@ __device__ __forceinline__ bool position(const QkArgs &A, int64_t t, int64_t &p)
     return false;
 }
 
+// The rows of a token whose position is outside the table: zeros.
 template <class T, int V, int K, int HPI>
-__global__ void __launch_bounds__(kQkWarps * 32)
+__device__ __forceinline__ void zero_token(const QkTensor &m, int64_t t, int h0, int ng,
+                                           const int (&at)[K], const int (&bt)[K],
+                                           const bool (&va)[K], const bool (&vb)[K])
+{
+    Vec<T, V> z;
+    zero_vec(z);
+#pragma unroll
+    for (int i = 0; i < HPI; ++i) {
+        const int h = h0 + i * ng;
+        T *row = static_cast<T *>(m.out) + t * m.out_t + h * m.out_h;
+#pragma unroll
+        for (int q = 0; q < K; ++q) {
+            if (h < m.H && va[q]) st_vec(row + at[q], z);
+            if (h < m.H && vb[q]) st_vec(row + bt[q], z);
+        }
+    }
+}
+
+// y = rho (x (gamma cos) + partner (gamma sin)): the products with gamma are
+// formed once per token and serve the set's heads.  MINB: blocks per SM that
+// the registers must leave room for.
+template <class T, int V, int K, int HPI, bool INTER, int MINB>
+__global__ void __launch_bounds__(kQkWarps * 32, MINB)
     k_qk_fwd(const __grid_constant__ QkArgs A, const __grid_constant__ QkGeom ge)
 {
+    typedef typename Elems<V>::E E;
+    constexpr int N = Elems<V>::N;
+    typedef Rope<V, INTER> R;
+    extern __shared__ __align__(16) float sg[];
     pdl_wait();
+    stage_gammas(A, sg);
     Work w;
     if (!my_work(ge, w)) return;
     const QkTensor &m = A.m[w.which];
+    const float *gam = sg + (w.which ? gamma_row(A.D) : 0);
     const int lane = threadIdx.x & 31, G = 1 << ge.lg, l = lane & (G - 1);
     const int ng = 32 >> ge.lg, h0 = w.set * (ng * HPI) + (lane >> ge.lg);
     const int half = A.R / 2, hr = half / V;
-    const bool inter = A.interleaved != 0;
     const float inv_d = 1.f / float(A.D);
     int at[K], bt[K];
     bool va[K], vb[K];
-    float ga[K][V], gb[K][V];
 #pragma unroll
     for (int q = 0; q < K; ++q) {
-        unit_at<V>(l + q * G, hr, half, inter, at[q], bt[q]);
+        unit_at<V>(l + q * G, hr, half, A.interleaved != 0, at[q], bt[q]);
         va[q] = at[q] < A.D;
         vb[q] = bt[q] < A.D;
-        load_gamma<V>(m.gamma, at[q], va[q], ga[q]);
-        load_gamma<V>(m.gamma, bt[q], vb[q], gb[q]);
     }
     for (int64_t t = w.t; t < A.T; t += ge.t_step) {
         Vec<T, V> xa[HPI][K], xb[HPI][K];
@@ -172,45 +233,74 @@ __global__ void __launch_bounds__(kQkWarps * 32)
             }
         }
         int64_t p;
-        const bool ok = position(A, t, p);
-        float c[K][V], s[K][V];
+        if (!position(A, t, p)) {
+            zero_token<T, V, K, HPI>(m, t, h0, ng, at, bt, va, vb);
+            continue;
+        }
+        E ca[K][N], cb[K][N], sa[K][N], sb[K][N];
 #pragma unroll
-        for (int q = 0; q < K; ++q)
-            if (ok && l + q * G < hr)
-                load_rope<V>(A.cs, A.sn, p * half + V * (l + q * G), c[q], s[q]);
+        for (int q = 0; q < K; ++q) {
+            E ga[N], gb[N];
+            gamma_e<V>(gam + (va[q] ? at[q] : 0), ga);
+            gamma_e<V>(gam + (vb[q] ? bt[q] : 0), gb);
+            if (l + q * G < hr) {
+                R r;
+                r.load(A.cs, A.sn, p * half + V * (l + q * G));
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    ca[q][e] = e_mul(ga[e], r.ca(e));
+                    cb[q][e] = e_mul(gb[e], r.cb(e));
+                    sa[q][e] = e_mul(R::pa(ga, gb, e), r.sa(e));
+                    sb[q][e] = e_mul(R::pb(ga, gb, e), r.sb(e));
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    ca[q][e] = ga[e];
+                    cb[q][e] = gb[e];
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < HPI; ++i) {
             const int h = h0 + i * ng;
-            float ss = 0.f;
+            E a[K][N], b[K][N], ss;
+            e_set(ss, 0.f);
 #pragma unroll
             for (int q = 0; q < K; ++q) {
-                float a[V], b[V];
-                widen(xa[i][q], a);
-                widen(xb[i][q], b);
+                widen_e<T, V>(xa[i][q], a[q]);
+                widen_e<T, V>(xb[i][q], b[q]);
 #pragma unroll
-                for (int e = 0; e < V; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+                for (int e = 0; e < N; ++e) ss = e_fma(a[q][e], a[q][e], e_fma(b[q][e], b[q][e], ss));
             }
-            ss = group_sum(ss, G);
-            const float den = ss * inv_d + A.eps;
-            // an all-zero head with eps = 0 gives zeros; an invalid position too
-            const float rho = den == 0.f || !ok ? 0.f : rsqrtf(den);
+            const float den = fmaf(group_sum(e_sum(ss), G), inv_d, A.eps);
+            const float rho = den == 0.f ? 0.f : rsqrtf(den);  // an all-zero head, eps = 0: zeros
             if (h >= m.H) continue;
+            E rr;
+            e_set(rr, rho);
             T *row = static_cast<T *>(m.out) + t * m.out_t + h * m.out_h;
 #pragma unroll
             for (int q = 0; q < K; ++q) {
-                float a[V], b[V];
-                widen(xa[i][q], a);
-                widen(xb[i][q], b);
+                E ya[N], yb[N];
+                if (l + q * G < hr) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    a[e] = ok ? a[e] * rho * ga[q][e] : 0.f;
-                    b[e] = ok ? b[e] * rho * gb[q][e] : 0.f;
+                    for (int e = 0; e < N; ++e) {
+                        ya[e] = e_mul(rr, e_fma(R::pa(a[q], b[q], e), sa[q][e],
+                                                e_mul(a[q][e], ca[q][e])));
+                        yb[e] = e_mul(rr, e_fma(R::pb(a[q], b[q], e), sb[q][e],
+                                                e_mul(b[q][e], cb[q][e])));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        ya[e] = e_mul(rr, e_mul(a[q][e], ca[q][e]));
+                        yb[e] = e_mul(rr, e_mul(b[q][e], cb[q][e]));
+                    }
                 }
-                if (ok && l + q * G < hr) rotate<V>(a, b, c[q], s[q], inter, 1.f);
                 Vec<T, V> o;
-                narrow(a, o);
+                narrow_e<T, V>(ya, o);
                 if (va[q]) st_vec(row + at[q], o);
-                narrow(b, o);
+                narrow_e<T, V>(yb, o);
                 if (vb[q]) st_vec(row + bt[q], o);
             }
         }
@@ -218,38 +308,44 @@ __global__ void __launch_bounds__(kQkWarps * 32)
 }
 
 // dgp: [gridDim.x][2][D] partial sums of dgamma, one row per block.
-template <class T, int V, int K, int HPI>
-__global__ void __launch_bounds__(kQkWarps * 32)
+template <class T, int V, int K, int HPI, bool INTER, int MINB>
+__global__ void __launch_bounds__(kQkWarps * 32, MINB)
     k_qk_bwd(const __grid_constant__ QkArgs A, const __grid_constant__ QkGeom ge,
              float *__restrict__ dgp)
 {
-    extern __shared__ float sm[];  // [kQkWarps][D]: a warp's dgamma partial
+    typedef typename Elems<V>::E E;
+    constexpr int N = Elems<V>::N;
+    typedef Rope<V, INTER> R;
+    extern __shared__ __align__(16) float sm[];  // gammas, then [kQkWarps][D] dgamma partials
     __shared__ int owner[kQkWarps];
     pdl_wait();
+    stage_gammas(A, sm);
+    float *part = sm + 2 * gamma_row(A.D);
     Work w;
     const bool active = my_work(ge, w);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = 1 << ge.lg, l = lane & (G - 1);
     const int ng = 32 >> ge.lg;
     const int half = A.R / 2, hr = half / V;
-    const bool inter = A.interleaved != 0;
     const float inv_d = 1.f / float(A.D);
     if (lane == 0) owner[warp] = active ? w.which : -1;
     if (active) {
         const QkTensor &m = A.m[w.which];
+        const float *gam = sm + (w.which ? gamma_row(A.D) : 0);
         const int h0 = w.set * (ng * HPI) + (lane >> ge.lg);
         int at[K], bt[K];
         bool va[K], vb[K];
-        float ga[K][V], gb[K][V], da[K][V], db[K][V];
+        E da[K][N], db[K][N];
 #pragma unroll
         for (int q = 0; q < K; ++q) {
-            unit_at<V>(l + q * G, hr, half, inter, at[q], bt[q]);
+            unit_at<V>(l + q * G, hr, half, A.interleaved != 0, at[q], bt[q]);
             va[q] = at[q] < A.D;
             vb[q] = bt[q] < A.D;
-            load_gamma<V>(m.gamma, at[q], va[q], ga[q]);
-            load_gamma<V>(m.gamma, bt[q], vb[q], gb[q]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) da[q][e] = db[q][e] = 0.f;
+            for (int e = 0; e < N; ++e) {
+                e_set(da[q][e], 0.f);
+                e_set(db[q][e], 0.f);
+            }
         }
         for (int64_t t = w.t; t < A.T; t += ge.t_step) {
             Vec<T, V> xa[HPI][K], xb[HPI][K], ya[HPI][K], yb[HPI][K];
@@ -268,71 +364,105 @@ __global__ void __launch_bounds__(kQkWarps * 32)
                 }
             }
             int64_t p;
-            const bool ok = position(A, t, p);
-            float c[K][V], s[K][V];
+            if (!position(A, t, p)) {
+                zero_token<T, V, K, HPI>(m, t, h0, ng, at, bt, va, vb);
+                continue;
+            }
+            R r[K];
 #pragma unroll
             for (int q = 0; q < K; ++q)
-                if (ok && l + q * G < hr)
-                    load_rope<V>(A.cs, A.sn, p * half + V * (l + q * G), c[q], s[q]);
+                if (l + q * G < hr) r[q].load(A.cs, A.sn, p * half + V * (l + q * G));
 #pragma unroll
             for (int i = 0; i < HPI; ++i) {
                 const int h = h0 + i * ng;
-                float s1 = 0.f, s2 = 0.f;  // sum x^2, sum g x
-                float a[K][V], b[K][V], u[K][V], v[K][V];
+                E s1, s2;  // sum x^2, sum g x
+                e_set(s1, 0.f);
+                e_set(s2, 0.f);
+                E a[K][N], b[K][N], u[K][N], v[K][N];  // x, then the upstream rotated back
 #pragma unroll
                 for (int q = 0; q < K; ++q) {
-                    widen(xa[i][q], a[q]);
-                    widen(xb[i][q], b[q]);
-                    widen(ya[i][q], u[q]);
-                    widen(yb[i][q], v[q]);
-                    if (ok && l + q * G < hr) rotate<V>(u[q], v[q], c[q], s[q], inter, -1.f);
+                    E ga[N], gb[N];
+                    gamma_e<V>(gam + (va[q] ? at[q] : 0), ga);
+                    gamma_e<V>(gam + (vb[q] ? bt[q] : 0), gb);
+                    widen_e<T, V>(xa[i][q], a[q]);
+                    widen_e<T, V>(xb[i][q], b[q]);
+                    widen_e<T, V>(ya[i][q], u[q]);
+                    widen_e<T, V>(yb[i][q], v[q]);
+                    if (l + q * G < hr) {
+                        E ru[N], rv[N];
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        s1 = fmaf(a[q][e], a[q][e], fmaf(b[q][e], b[q][e], s1));
-                        s2 = fmaf(u[q][e] * ga[q][e], a[q][e],
-                                  fmaf(v[q][e] * gb[q][e], b[q][e], s2));
+                        for (int e = 0; e < N; ++e) {
+                            ru[e] = e_fma(R::pa(u[q], v[q], e), e_neg(r[q].sa(e)),
+                                          e_mul(u[q][e], r[q].ca(e)));
+                            rv[e] = e_fma(R::pb(u[q], v[q], e), e_neg(r[q].sb(e)),
+                                          e_mul(v[q][e], r[q].cb(e)));
+                        }
+#pragma unroll
+                        for (int e = 0; e < N; ++e) {
+                            u[q][e] = ru[e];
+                            v[q][e] = rv[e];
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        s1 = e_fma(a[q][e], a[q][e], e_fma(b[q][e], b[q][e], s1));
+                        s2 = e_fma(e_mul(u[q][e], ga[e]), a[q][e],
+                                   e_fma(e_mul(v[q][e], gb[e]), b[q][e], s2));
                     }
                 }
-                s1 = group_sum(s1, G);
-                s2 = group_sum(s2, G);
-                const float den = s1 * inv_d + A.eps;
-                const float rho = den == 0.f || !ok ? 0.f : rsqrtf(den);
-                const float k2 = s2 * rho * inv_d;  // mean of g xh
+                const float den = fmaf(group_sum(e_sum(s1), G), inv_d, A.eps);
+                const float rho = den == 0.f ? 0.f : rsqrtf(den);
+                const float k2 = group_sum(e_sum(s2), G) * rho * inv_d;  // mean of g xh
                 if (h >= m.H) continue;
+                E rr, nk;
+                e_set(rr, rho);
+                e_set(nk, -k2);
                 T *row = static_cast<T *>(m.out) + t * m.out_t + h * m.out_h;
 #pragma unroll
                 for (int q = 0; q < K; ++q) {
-                    float o1[V], o2[V];
+                    E ga[N], gb[N], o1[N], o2[N];
+                    gamma_e<V>(gam + (va[q] ? at[q] : 0), ga);
+                    gamma_e<V>(gam + (vb[q] ? bt[q] : 0), gb);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const float xa_ = a[q][e] * rho, xb_ = b[q][e] * rho;
-                        o1[e] = ok ? rho * (u[q][e] * ga[q][e] - xa_ * k2) : 0.f;
-                        o2[e] = ok ? rho * (v[q][e] * gb[q][e] - xb_ * k2) : 0.f;
-                        if (ok) {
-                            da[q][e] = fmaf(u[q][e], xa_, da[q][e]);
-                            db[q][e] = fmaf(v[q][e], xb_, db[q][e]);
-                        }
+                    for (int e = 0; e < N; ++e) {
+                        const E ha = e_mul(a[q][e], rr), hb = e_mul(b[q][e], rr);
+                        o1[e] = e_mul(rr, e_fma(ha, nk, e_mul(u[q][e], ga[e])));
+                        o2[e] = e_mul(rr, e_fma(hb, nk, e_mul(v[q][e], gb[e])));
+                        da[q][e] = e_fma(u[q][e], ha, da[q][e]);
+                        db[q][e] = e_fma(v[q][e], hb, db[q][e]);
                     }
                     Vec<T, V> o;
-                    narrow(o1, o);
+                    narrow_e<T, V>(o1, o);
                     if (va[q]) st_vec(row + at[q], o);
-                    narrow(o2, o);
+                    narrow_e<T, V>(o2, o);
                     if (vb[q]) st_vec(row + bt[q], o);
                 }
             }
         }
         if (dgp) {
 #pragma unroll
-            for (int q = 0; q < K; ++q)
+            for (int q = 0; q < K; ++q) {
+                float fa[V], fb[V];
+                if constexpr (V == 1) {
+                    fa[0] = da[q][0];
+                    fb[0] = db[q][0];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) {
+                        f2_split(da[q][e], fa[2 * e], fa[2 * e + 1]);
+                        f2_split(db[q][e], fb[2 * e], fb[2 * e + 1]);
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     for (int x = 16; x >= G; x >>= 1) {
-                        da[q][e] += __shfl_xor_sync(kFull, da[q][e], x);
-                        db[q][e] += __shfl_xor_sync(kFull, db[q][e], x);
+                        fa[e] += __shfl_xor_sync(kFull, fa[e], x);
+                        fb[e] += __shfl_xor_sync(kFull, fb[e], x);
                     }
-                    if (lane < G && va[q]) sm[warp * A.D + at[q] + e] = da[q][e];
-                    if (lane < G && vb[q]) sm[warp * A.D + bt[q] + e] = db[q][e];
+                    if (lane < G && va[q]) part[warp * A.D + at[q] + e] = fa[e];
+                    if (lane < G && vb[q]) part[warp * A.D + bt[q] + e] = fb[e];
                 }
+            }
         }
     }
     if (!dgp) return;
@@ -342,31 +472,35 @@ __global__ void __launch_bounds__(kQkWarps * 32)
         const int which = i >= A.D, d = which ? i - A.D : i;
         float v = 0.f;
         for (int k = 0; k < kQkWarps; ++k)
-            if (owner[k] == which) v += sm[k * A.D + d];
+            if (owner[k] == which) v += part[k * A.D + d];
         dgp[int64_t(blockIdx.x) * 2 * A.D + i] = v;
     }
 }
 
-// dgamma[d] = sum of the blocks' partials in a fixed order: thread (x, y) of
-// a 32 x 32 block adds rows y, y + 32, ... of its column, then the 32 sums
-// are added in ascending y.
+// dgamma[d] = sum of the blocks' partials in a fixed order.  A block has 8
+// columns; thread (x, y) adds rows y, y + 128, ... of column x, and the 128
+// sums of a column are added by one warp.
 __global__ void __launch_bounds__(1024)
     k_qk_dgamma(const float *__restrict__ part, int rows, int D, float *__restrict__ dgq,
                 float *__restrict__ dgk)
 {
     pdl_wait();
-    __shared__ float red[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x;
+    __shared__ float red[8][128];
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3, c = blockIdx.x * 8 + x;
     float s = 0.f;
     if (c < 2 * D)
-        for (int r = threadIdx.y; r < rows; r += 32) s += part[int64_t(r) * 2 * D + c];
-    red[threadIdx.y][threadIdx.x] = s;
+#pragma unroll 4
+        for (int r = y; r < rows; r += 128) s += __ldg(part + int64_t(r) * 2 * D + c);
+    red[x][y] = s;
     __syncthreads();
-    if (threadIdx.y == 0 && c < 2 * D) {
-        float t = 0.f;
-        for (int g = 0; g < 32; ++g) t += red[g][threadIdx.x];
-        float *out = c < D ? dgq : dgk;
-        if (out) out[c < D ? c : c - D] = t;
+    const int lane = threadIdx.x & 31, col = threadIdx.x >> 5;
+    if (col >= 8) return;
+    const float t = warp_sum((red[col][lane] + red[col][lane + 32]) +
+                             (red[col][lane + 64] + red[col][lane + 96]));
+    const int d = blockIdx.x * 8 + col;
+    if (lane == 0 && d < 2 * D) {
+        float *out = d < D ? dgq : dgk;
+        if (out) out[d < D ? d : d - D] = t;
     }
 }
 
@@ -395,8 +529,9 @@ int qk_vec(const QkArgs &a, int es)
     return 1;
 }
 
-constexpr int kQkMaxBlocks = kSplitSms * 4;     // forward: four blocks of 8 warps per SM
-constexpr int kQkBwdMaxBlocks = kSplitSms * 2;  // backward: two
+// Blocks of a launch: as many as stay resident, MINB per SM.
+constexpr int qk_blocks(int minb) { return kSplitSms * minb; }
+constexpr int kQkBwdMaxBlocks = qk_blocks(4);  // what the workspace allows for
 
 QkGeom qk_geom(const QkArgs &a, int V, int hpi, int max_blocks, int *blocks)
 {
@@ -418,45 +553,59 @@ QkGeom qk_geom(const QkArgs &a, int V, int hpi, int max_blocks, int *blocks)
 // Enough warps to fill the SMs even with one head (per lane group) a warp?
 bool qk_many(const QkArgs &a) { return a.T * (a.m[0].H + a.m[1].H) >= int64_t(kSplitSms) * 64; }
 
-template <class T, int V, int K, int HPI>
+template <class T, int V, int K, int HPI, int MINB>
 cudaError_t run_fwd(const QkArgs &a, cudaStream_t s)
 {
     int blocks;
-    const QkGeom g = qk_geom(a, V, HPI, kQkMaxBlocks, &blocks);
+    const QkGeom g = qk_geom(a, V, HPI, qk_blocks(MINB), &blocks);
+    const size_t smem = size_t(2) * ((a.D + 7) & ~7) * sizeof(float);
+    auto kernel = V > 1 && a.interleaved ? k_qk_fwd<T, V, K, HPI, (V > 1), MINB>
+                                         : k_qk_fwd<T, V, K, HPI, false, MINB>;
     MHC_PROF("k_qk_fwd", s);
-    return launch_k(k_qk_fwd<T, V, K, HPI>, dim3(unsigned(blocks)), dim3(kQkWarps * 32), 0, s, a, g);
+    return launch_k(kernel, dim3(unsigned(blocks)), dim3(kQkWarps * 32), smem, s, a, g);
 }
 
-template <class T, int V, int K, int HPI>
+template <class T, int V, int K, int HPI, int MINB>
 cudaError_t run_bwd(const QkArgs &a, float *ws, cudaStream_t s)
 {
+    static_assert(qk_blocks(MINB) <= kQkBwdMaxBlocks, "the workspace has a row per block");
     int blocks;
-    const QkGeom g = qk_geom(a, V, HPI, kQkBwdMaxBlocks, &blocks);
+    const QkGeom g = qk_geom(a, V, HPI, qk_blocks(MINB), &blocks);
     float *part = a.m[0].dgamma || a.m[1].dgamma ? ws : nullptr;
-    const size_t smem = part ? size_t(kQkWarps) * a.D * sizeof(float) : 0;
+    const size_t smem = (size_t(2) * ((a.D + 7) & ~7) + (part ? size_t(kQkWarps) * a.D : 0)) *
+                        sizeof(float);
+    auto kernel = V > 1 && a.interleaved ? k_qk_bwd<T, V, K, HPI, (V > 1), MINB>
+                                         : k_qk_bwd<T, V, K, HPI, false, MINB>;
     {
         MHC_PROF("k_qk_bwd", s);
-        const cudaError_t e = launch_k(k_qk_bwd<T, V, K, HPI>, dim3(unsigned(blocks)),
-                                       dim3(kQkWarps * 32), smem, s, a, g, part);
+        const cudaError_t e = launch_k(kernel, dim3(unsigned(blocks)), dim3(kQkWarps * 32), smem, s,
+                                       a, g, part);
         if (e != cudaSuccess || !part) return e;
     }
     MHC_PROF("k_qk_dgamma", s);
-    return launch_k(k_qk_dgamma, dim3(unsigned((2 * a.D + 31) / 32)), dim3(32, 32), 0, s, part,
-                    blocks, a.D, a.m[0].dgamma, a.m[1].dgamma);
+    return launch_k(k_qk_dgamma, dim3(unsigned((2 * a.D + 7) / 8)), dim3(1024), 0, s, part, blocks,
+                    a.D, a.m[0].dgamma, a.m[1].dgamma);
 }
+
+// Heads per lane group and blocks per SM of the 16-byte forms on long inputs.
+// 16384 tokens of 32 + 8 heads of 128, bf16: forward 2, 3 take 56.2 us; 4, 3
+// (spills) 59.2; 4, 2 64.3; 1, 4 62.4.  Backward 2, 2 take 95.0; 1, 2 108;
+// 1, 3 122.
+constexpr int kFwdHeads = 2, kFwdBlocks = 3, kBwdHeads = 2, kBwdBlocks = 2;
 
 template <class T>
 cudaError_t fwd_of(const QkArgs &a, cudaStream_t s)
 {
     switch (qk_vec(a, int(sizeof(T)))) {
     case 8:
-        return qk_many(a) ? run_fwd<T, 8, 1, (sizeof(T) == 4 ? 2 : 4)>(a, s)
-                          : run_fwd<T, 8, 1, 1>(a, s);
+        if (!qk_many(a)) return run_fwd<T, 8, 1, 1, 3>(a, s);
+        if constexpr (sizeof(T) == 4) return run_fwd<T, 8, 1, 2, 3>(a, s);
+        else return run_fwd<T, 8, 1, kFwdHeads, kFwdBlocks>(a, s);
     case 2:
-        if (a.D > 128) return run_fwd<T, 2, 4, 1>(a, s);
-        return qk_many(a) ? run_fwd<T, 2, 1, 4>(a, s) : run_fwd<T, 2, 1, 1>(a, s);
+        if (a.D > 128) return run_fwd<T, 2, 4, 1, 2>(a, s);
+        return qk_many(a) ? run_fwd<T, 2, 1, 4, 4>(a, s) : run_fwd<T, 2, 1, 1, 4>(a, s);
     default:
-        return a.D > 128 ? run_fwd<T, 1, 8, 1>(a, s) : run_fwd<T, 1, 2, 2>(a, s);
+        return a.D > 128 ? run_fwd<T, 1, 8, 1, 2>(a, s) : run_fwd<T, 1, 2, 2, 3>(a, s);
     }
 }
 
@@ -465,13 +614,14 @@ cudaError_t bwd_of(const QkArgs &a, float *ws, cudaStream_t s)
 {
     switch (qk_vec(a, int(sizeof(T)))) {
     case 8:
-        return qk_many(a) && sizeof(T) == 2 ? run_bwd<T, 8, 1, 2>(a, ws, s)
-                                            : run_bwd<T, 8, 1, 1>(a, ws, s);
+        if constexpr (sizeof(T) == 2)
+            if (qk_many(a)) return run_bwd<T, 8, 1, kBwdHeads, kBwdBlocks>(a, ws, s);
+        return run_bwd<T, 8, 1, 1, 2>(a, ws, s);
     case 2:
-        if (a.D > 128) return run_bwd<T, 2, 4, 1>(a, ws, s);
-        return qk_many(a) ? run_bwd<T, 2, 1, 4>(a, ws, s) : run_bwd<T, 2, 1, 1>(a, ws, s);
+        if (a.D > 128) return run_bwd<T, 2, 4, 1, 2>(a, ws, s);
+        return qk_many(a) ? run_bwd<T, 2, 1, 4, 3>(a, ws, s) : run_bwd<T, 2, 1, 1, 3>(a, ws, s);
     default:
-        return a.D > 128 ? run_bwd<T, 1, 8, 1>(a, ws, s) : run_bwd<T, 1, 2, 2>(a, ws, s);
+        return a.D > 128 ? run_bwd<T, 1, 8, 1, 1>(a, ws, s) : run_bwd<T, 1, 2, 2, 2>(a, ws, s);
     }
 }
 
