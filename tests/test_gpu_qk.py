@@ -134,6 +134,40 @@ def test_layouts_give_the_contiguous_result(M, D, R, dt):
     O.check(a, ref, mag, D / 2 + 12, "broadcast")
 
 
+# long inputs (the walk over tokens): the largest head, heads that fill their
+# lanes and heads that do not, more heads than lanes, both pairings
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,Hq,Hk,D,R,inter", [
+    (2500, 3, 1, 512, 512, False), (2450, 4, 0, 64, 64, True), (203, 70, 5, 16, 16, False),
+    (611, 14, 2, 96, 96, True), (305, 33, 0, 256, 256, False), (1300, 7, 1, 128, 48, False),
+    (401, 24, 3, 80, 20, False)])
+def test_long_inputs_in_any_layout(M, T, Hq, Hk, D, R, inter, dt):
+    d = make(T, Hq, Hk, D, R, dt, seed=8)
+    d["pos"][T // 2] = 97  # one token without a place in the table
+    qo, ko = run_fwd(M, d, inter)
+    dq, dk, dgq, dgk = run_bwd(M, d, inter)
+    assert M.mhc_device_error() == 201
+    at = d["pos"].long().cpu().numpy()
+    cos, sin = (O.np64(d[n])[np.minimum(at, 96)] for n in ("cos", "sin"))
+    keep = np.arange(T) != T // 2
+    for y, gy, gg, x, u, g, H in ((qo, dq, dgq, "q", "dq", "gq", Hq), (ko, dk, dgk, "k", "dk", "gk", Hk)):
+        args = O.np64(d[x])[keep], O.np64(d[g]), cos[keep], sin[keep], R, inter, EPS
+        assert torch.all(y[T // 2] == 0) and torch.all(gy[T // 2] == 0)
+        k = torch.from_numpy(keep).cuda()
+        O.check(y[k], *O.qk_fwd(*args), D / 2 + 12, x)
+        dx, dxm, dg, dgm = O.qk_bwd(O.np64(d[u])[keep], *args)
+        O.check(gy[k], dx, dxm, 2 * D + 20, "d" + x)
+        O.check(gg, dg, dgm, T * H + D + 20, "dgamma " + x)
+    # head-major inputs and outputs
+    major = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)  # noqa: E731
+    e = dict(d, **{n: major(d[n]) for n in ("q", "k", "dq", "dk")})
+    a, b = run_fwd(M, e, inter, qo=major(qo), ko=major(ko))
+    assert torch.equal(a, qo) and torch.equal(b, ko)
+    for x, y in zip(run_bwd(M, e, inter, major(dq), major(dk)), (dq, dk, dgq, dgk)):
+        assert torch.equal(x, y)
+    M.mhc_device_error()
+
+
 def test_no_gamma_no_positions_no_rotation_no_k(M):
     d = make(5, 3, 2, 64, 64, torch.bfloat16, seed=3)
     plain = dict(d, gq=None, gk=None, pos=None)
