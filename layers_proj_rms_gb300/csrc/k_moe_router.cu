@@ -28,7 +28,7 @@ constexpr int kFaultChoice = 204;  // backward: an id outside [-1, E)
 
 namespace {
 
-constexpr int kRouterWarps = 4;
+constexpr int kRouterWarps = 4;  // 8: within 2%; 16: 20% slower
 
 __device__ __forceinline__ float warp_max(float v)
 {
@@ -44,12 +44,12 @@ __device__ __forceinline__ void narrow1(float f, bf16 &o) { o = __float2bfloat16
 __device__ __forceinline__ void narrow1(float f, fp16 &o) { o = __float2half_rn(f); }
 __device__ __forceinline__ void narrow1(float f, float &o) { o = f; }
 
-// Ascending integer key of a float; > 0; equal for -0 and 0; NaN the largest.
+// Ascending integer key of a float; > 0; equal for -0 and 0; NaN the largest
+// (the sum with 0 turns -0 into 0 and every NaN into the canonical 0x7fffffff).
 __device__ __forceinline__ unsigned key_of(float f)
 {
-    if (f != f) return 0xffffffffu;
-    const unsigned u = __float_as_uint(f + 0.f);
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const unsigned u = __float_as_uint(__fadd_rn(f, 0.f));
+    return u ^ (unsigned(int(u) >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ float logistic(float l) { return 1.f / (1.f + expf(-l)); }
@@ -68,13 +68,35 @@ __device__ __forceinline__ float lane_softmax(float v, bool on)
     return s == 0.f ? 0.f : p / s;
 }
 
-template <class T, int NV>
+// A lane's NV logits.  FULL (E = 32 NV): runs of up to eight neighbours, loaded
+// as vectors; else one of every 32.
+template <int NV, bool FULL>
+__device__ __forceinline__ int expert_of(int lane, int i)
+{
+    constexpr int RUN = NV < 8 ? NV : 8;
+    return FULL ? (i / RUN * 32 + lane) * RUN + i % RUN : lane + 32 * i;
+}
+
+template <class T, int NV, bool FULL>
 __device__ __forceinline__ void load_row(const T *row, int E, int lane, float (&l)[NV])
 {
+    constexpr int RUN = NV < 8 ? NV : 8;
+    if constexpr (FULL) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < E ? widen1(row[e]) : -INFINITY;
+        for (int i = 0; i < NV; i += RUN) {
+            Vec<T, RUN> v;
+            float f[RUN];
+            ld_vec(v, row + expert_of<NV, FULL>(lane, i));
+            widen(v, f);
+#pragma unroll
+            for (int e = 0; e < RUN; ++e) l[i + e] = f[e];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane + 32 * i;
+            l[i] = e < E ? widen1(row[e]) : -INFINITY;
+        }
     }
 }
 
@@ -128,13 +150,13 @@ __device__ __forceinline__ unsigned pack_of(float l, int e)
 }
 
 // Exact choice by whole keys, one maximum at a time: lane j gets choice j.
-template <int NV>
+template <int NV, bool FULL>
 __device__ __noinline__ int choose_exact(const float (&l)[NV], int E, int k)
 {
     const int lane = threadIdx.x & 31;
     unsigned key[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) key[i] = lane + 32 * i < E ? key_of(l[i]) : 0u;
+    for (int i = 0; i < NV; ++i) key[i] = FULL || lane + 32 * i < E ? key_of(l[i]) : 0u;
     int mine = 0;
     for (int j = 0; j < k; ++j) {
         unsigned best = 0u;
@@ -143,19 +165,19 @@ __device__ __noinline__ int choose_exact(const float (&l)[NV], int E, int k)
         for (int i = 0; i < NV; ++i)
             if (key[i] > best) {
                 best = key[i];
-                at = i;
+                at = expert_of<NV, FULL>(lane, i);
             }
         const unsigned top = __reduce_max_sync(kFull, best);
-        const int e = int(__reduce_min_sync(kFull, best == top ? unsigned(lane + 32 * at) : ~0u));
+        const int e = int(__reduce_min_sync(kFull, best == top ? unsigned(at) : ~0u));
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (e == lane + 32 * i) key[i] = 0u;
+            if (e == expert_of<NV, FULL>(lane, i)) key[i] = 0u;
         if (lane == j) mine = e;
     }
     return mine;
 }
 
-template <class T, int NV>
+template <class T, int NV, bool FULL>
 __global__ void __launch_bounds__(kRouterWarps * 32)
     k_moe_router(const T *__restrict__ logits, int64_t tokens, int E, int k, int score,
                  int renorm, float scale, int32_t *__restrict__ ids, float *__restrict__ w)
@@ -166,26 +188,26 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
     if (t >= tokens) return;
     const T *row = logits + t * E;
     float l[NV];
-    load_row<T, NV>(row, E, lane, l);
+    load_row<T, NV, FULL>(row, E, lane, l);
     unsigned p[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-        p[i] = lane + 32 * i < E ? pack_of(l[i], lane + 32 * i) : 0u;
+        p[i] = FULL || lane + 32 * i < E ? pack_of(l[i], expert_of<NV, FULL>(lane, i)) : 0u;
     // up to eight values a lane are sorted, so that a round only looks at the
     // head; more are searched in every round
     constexpr bool kSorted = NV <= 8;
     if constexpr (kSorted) sort_desc<NV>(p);
-    unsigned mine = 0u, last = 0u;
-    bool sure = true;
+    unsigned mine = 0u, last = 0u;  // choice `lane`; the last one
     const int rounds = sizeof(T) == 2 || k == E ? k : k + 1;
+#pragma unroll 3
     for (int j = 0; j < rounds; ++j) {
         unsigned best = p[0];
         if constexpr (!kSorted)
 #pragma unroll
             for (int i = 1; i < NV; ++i) best = max(best, p[i]);
-        const unsigned top = __reduce_max_sync(kFull, best);
+        last = __reduce_max_sync(kFull, best);
         if constexpr (kSorted) {
-            if (p[0] == top) {
+            if (p[0] == last) {
 #pragma unroll
                 for (int i = 0; i + 1 < NV; ++i) p[i] = p[i + 1];
                 p[NV - 1] = 0u;
@@ -193,19 +215,28 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                if (p[i] == top) p[i] = 0u;
+                if (p[i] == last) p[i] = 0u;
         }
-        if (sizeof(T) == 4) sure = sure && (j == 0 || (top ^ last) >= 1024u);
-        last = top;
-        if (lane == j) mine = top;
+        if (lane == j) mine = last;
     }
-    int my_id = 1023 - int(mine & 1023u);
-    if (sizeof(T) == 4 && !sure) my_id = choose_exact<NV>(l, E, k);
     const bool on = lane < k;
+    int my_id = 1023 - int(mine & 1023u);
+    if constexpr (sizeof(T) == 4) {
+        // neighbours in order: lanes 0 .. k - 1, then the one after them
+        const unsigned next = __shfl_down_sync(kFull, mine, 1);
+        const bool near = on && (mine ^ (lane == k - 1 ? last : next)) < 1024u;
+        if (__any_sync(kFull, near && !(lane == k - 1 && rounds == k)))
+            my_id = choose_exact<NV, FULL>(l, E, k);
+    }
     const float my_l = on ? widen1(row[my_id]) : -INFINITY;
     float v;
     if (renorm) {
-        v = lane_softmax(score == 0 ? my_l : log_logistic(my_l), on);
+        // lane 0 has the largest
+        const float s = score == 0 ? my_l : log_logistic(my_l);
+        const float m = __shfl_sync(kFull, s, 0);
+        v = on && m != -INFINITY ? expf(s - m) : 0.f;
+        const float sum = warp_sum(v);
+        v = sum == 0.f ? 0.f : v / sum;
     } else if (score == 0) {
         float m, sum;
         row_stats<NV>(l, m, sum);
@@ -248,7 +279,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
         if (score != 0) d *= logistic(-lj);
     } else if (score == 0) {
         float l[NV], m, sum;
-        load_row<T, NV>(row, E, lane, l);
+        load_row<T, NV, false>(row, E, lane, l);
         row_stats<NV>(l, m, sum);
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const float v = on ? expf(lj - m) * inv : 0.f;
@@ -288,7 +319,9 @@ cudaError_t fwd_of(const void *logits, int64_t tokens, int E, int k, int score, 
                    float scale, int32_t *ids, float *w, cudaStream_t s)
 {
     const dim3 g(unsigned((tokens + kRouterWarps - 1) / kRouterWarps));
-    MHC_ROUTER_NV(NV, return launch_k(k_moe_router<T, NV>, g, dim3(kRouterWarps * 32), 0, s,
+    MHC_ROUTER_NV(NV, return launch_k(E == 32 * NV ? k_moe_router<T, NV, true>
+                                                   : k_moe_router<T, NV, false>,
+                                      g, dim3(kRouterWarps * 32), 0, s,
                                       static_cast<const T *>(logits), tokens, E, k, score, renorm,
                                       scale, ids, w));
 }

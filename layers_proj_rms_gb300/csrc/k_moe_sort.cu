@@ -8,8 +8,8 @@
 //
 // One launch of one thread-block cluster.  The slots are cut into contiguous
 // segments, one per warp of the cluster.  Each warp counts its segment's
-// experts in shared memory: match_any groups the equal ids of 32 slots, and
-// the group's lowest lane adds its size, so no atomics and no order left open.
+// experts in shared memory: ballots group the equal ids of 32 slots, and the
+// group's lowest lane adds its size, so no atomics and no order left open.
 // What a slot found there before it is its rank in the segment.  The counts of
 // a block's warps are scanned per expert, the blocks' totals exchanged through
 // distributed shared memory, and one scan over the experts gives the offsets:
@@ -30,8 +30,9 @@ constexpr int kFaultExpert = 202;  // an expert id outside [-1, E)
 
 namespace {
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
+// Warps of a block: 8 for a few slots and experts (fewer to synchronise: 148
+// slots of 60 experts), else 32.
+constexpr int kFewWarps = 8, kSortWarps = 32;
 
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(kFull, v); }
 
@@ -62,14 +63,33 @@ __device__ __forceinline__ void load_tile(const SortArgs &A, int64_t b, int64_t 
         }
 }
 
+// All ones where bit b of e is set, else 0.
+__device__ __forceinline__ unsigned bit_mask(int e, int b)
+{
+    unsigned m;
+    asm("bfe.s32 %0, %1, %2, 1;" : "=r"(m) : "r"(e), "r"(b));
+    return m;
+}
+
 // Ranks of a tile's slots among the segment's slots of the same expert; mine
-// holds how many there were before, and is brought up to date.
-__device__ __forceinline__ void rank_tile(const int (&e)[kTile], int *mine, int lane, int (&rank)[kTile])
+// holds how many there were before, and is brought up to date.  The lanes of
+// equal ids are found by a ballot per bit of the id.
+__device__ __forceinline__ void rank_tile(const int (&e)[kTile], int bits, int *mine, int lane,
+                                          int (&rank)[kTile])
 {
     const unsigned below = (1u << lane) - 1u;
     unsigned same[kTile];
 #pragma unroll
-    for (int q = 0; q < kTile; ++q) same[q] = __match_any_sync(kFull, e[q]);
+    for (int q = 0; q < kTile; ++q) same[q] = __ballot_sync(kFull, e[q] >= 0);  // -1: not used
+#pragma unroll
+    for (int b = 0; b < 10; ++b) {  // E <= 1024
+        if (b >= bits) break;
+#pragma unroll
+        for (int q = 0; q < kTile; ++q) {
+            const unsigned m = __ballot_sync(kFull, e[q] & (1 << b));
+            same[q] &= ~(m ^ bit_mask(e[q], b));
+        }
+    }
 #pragma unroll
     for (int q = 0; q < kTile; ++q) {
         rank[q] = e[q] >= 0 ? mine[e[q]] + __popc(same[q] & below) : 0;
@@ -79,22 +99,24 @@ __device__ __forceinline__ void rank_tile(const int (&e)[kTile], int *mine, int 
     }
 }
 
-// ONE: every segment is one tile
-template <bool ONE>
-__global__ void __launch_bounds__(kSortThreads) k_moe_sort(const SortArgs A)
+// ONE: every segment is one tile.  W: warps of a block; E <= 32 W
+template <bool ONE, int W>
+__global__ void __launch_bounds__(32 * W) k_moe_sort(const SortArgs A)
 {
     extern __shared__ int sm[];
     const int E = A.E;
     int *hist = sm;                       // [warps][E], then exclusive over warps, plus base
-    int *total = hist + kSortWarps * E;   // [E] this block's counts (read by the cluster)
+    int *total = hist + W * E;   // [E] this block's counts (read by the cluster)
     int *base = total + E;                // [E] row of this block's first slot of e
     int *off = base + E;                  // [E + 1] padded offsets
     int *count = off + E + 1;             // [E] counts over all blocks
-    __shared__ int wsum[kSortWarps];
+    int *loc = count + E;                 // [E] this block's slots of lower experts
+    int *sorted = loc + E;                // [32 W kTile] ONE: the block's slots by expert
+    __shared__ int wsum[2][W];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = int(cluster.block_rank()), nb = int(cluster.num_blocks());
-    const int64_t gw = int64_t(rank) * kSortWarps + warp;
+    const int64_t gw = int64_t(rank) * W + warp;
     const int64_t s0 = gw * A.seg < A.N ? gw * A.seg : A.N;
     const int64_t s1 = s0 + A.seg < A.N ? s0 + A.seg : A.N;
     int *mine = hist + warp * E;
@@ -102,25 +124,26 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const SortArgs A)
     __syncwarp();
     pdl_wait();
 
+    const int bits = 32 - __clz(E - 1);  // of an id; 0 where E = 1
     int e[kTile], rk[kTile];
     for (int64_t b = s0; b < s1; b += 32 * kTile) {
         load_tile(A, b, s1, lane, e);
-        rank_tile(e, mine, lane, rk);
+        rank_tile(e, bits, mine, lane, rk);
     }
     __syncthreads();
-    for (int x = tid; x < E; x += kSortThreads) {
-        int c[kSortWarps], s = 0;
+    for (int x = tid; x < E; x += 32 * W) {
+        int c[W], s = 0;
 #pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) c[w] = hist[w * E + x];
+        for (int w = 0; w < W; ++w) c[w] = hist[w * E + x];
 #pragma unroll
-        for (int w = 0; w < kSortWarps; ++w) {
+        for (int w = 0; w < W; ++w) {
             hist[w * E + x] = s;
             s += c[w];
         }
         total[x] = s;
     }
     cluster.sync();
-    // E <= kSortThreads: thread x owns expert x
+    // E <= 32 * W: thread x owns expert x
     int all = 0, before = 0;
     if (tid < E)
 #pragma unroll 8
@@ -131,20 +154,27 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const SortArgs A)
         }
     // padded < 2^31: the caller has checked R
     const int padded = (all + A.align - 1) / A.align * A.align;
-    int incl = padded;
+    int incl = padded, here = tid < E ? total[tid] : 0, incl_here = here;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(kFull, incl, d);
-        if (lane >= d) incl += v;
+        const int v = __shfl_up_sync(kFull, incl, d), w = __shfl_up_sync(kFull, incl_here, d);
+        if (lane >= d) {
+            incl += v;
+            incl_here += w;
+        }
     }
-    if (lane == 31) wsum[warp] = incl;
+    if (lane == 31) {
+        wsum[0][warp] = incl;
+        wsum[1][warp] = incl_here;
+    }
     __syncthreads();
-    const int before_warps = warp_sum_int(lane < warp ? wsum[lane] : 0);
-    const int start = before_warps + incl - padded;
+    const int start = warp_sum_int(lane < warp ? wsum[0][lane] : 0) + incl - padded;
+    const int mine_from = warp_sum_int(lane < warp ? wsum[1][lane] : 0) + incl_here - here;
     if (tid < E) {
         off[tid] = start;
         base[tid] = start + before;
         count[tid] = all;
+        loc[tid] = mine_from;
         if (tid == E - 1) off[E] = start + padded;
         if (rank == 0) {
             A.counts[tid] = all;
@@ -155,27 +185,52 @@ __global__ void __launch_bounds__(kSortThreads) k_moe_sort(const SortArgs A)
     // also: nobody leaves while its totals are still being read
     cluster.sync();
 
-    for (int64_t b = s0; b < s1; b += 32 * kTile) {
-        if (!ONE) {
-            load_tile(A, b, s1, lane, e);
-            rank_tile(e, mine, lane, rk);
-        }
+    if constexpr (ONE) {
+        // rows in slot order; slots by expert into shared memory, from where
+        // neighbours of a segment leave together (straight to memory, each of
+        // 32 lanes to a line of its own, they took 5 us of 131072 slots' 14.6)
+        const int64_t block0 = int64_t(rank) * W * A.seg;
 #pragma unroll
         for (int q = 0; q < kTile; ++q) {
-            const int64_t i = b + 32 * q + lane;
+            const int64_t i = s0 + 32 * q + lane;
             if (i < s1) {
-                const int row = e[q] < 0 ? -1 : base[e[q]] + rk[q] + (ONE ? mine[e[q]] : 0);
-                A.row_of[i] = row;
-                if (row >= 0) A.slot_of[row] = int(i);
+                const int x = e[q], r = x < 0 ? 0 : mine[x] + rk[q];
+                A.row_of[i] = x < 0 ? -1 : base[x] + r;
+                if (x >= 0) sorted[loc[x] + r] = int(i - block0) << 10 | x;
+            }
+        }
+        __syncthreads();
+        const int n = loc[E - 1] + total[E - 1];
+        for (int i = tid; i < n; i += 32 * W) {
+            const int x = sorted[i] & 1023;
+            A.slot_of[base[x] + i - loc[x]] = int(block0) + (sorted[i] >> 10);
+        }
+    } else {
+        for (int64_t b = s0; b < s1; b += 32 * kTile) {
+            load_tile(A, b, s1, lane, e);
+            rank_tile(e, bits, mine, lane, rk);
+#pragma unroll
+            for (int q = 0; q < kTile; ++q) {
+                const int64_t i = b + 32 * q + lane;
+                if (i < s1) {
+                    const int row = e[q] < 0 ? -1 : base[e[q]] + rk[q];
+                    A.row_of[i] = row;
+                    if (row >= 0) A.slot_of[row] = int(i);
+                }
             }
         }
     }
     // padding of the segments, then the rows past the last one
-    for (int e = int(gw); e < E; e += nb * kSortWarps)
+    for (int e = int(gw); e < E; e += nb * W)
         for (int r = off[e] + count[e] + lane; r < off[e + 1]; r += 32) A.slot_of[r] = -1;
-    for (int64_t r = off[E] + int64_t(rank) * kSortThreads + tid; r < A.R;
-         r += int64_t(nb) * kSortThreads)
+    for (int64_t r = off[E] + int64_t(rank) * (32 * W) + tid; r < A.R;
+         r += int64_t(nb) * (32 * W))
         A.slot_of[r] = -1;
+}
+
+size_t sort_smem(int E, bool one, int warps)
+{
+    return (size_t(warps + 5) * E + 1 + (one ? warps * 32 * kTile : 0)) * sizeof(int);
 }
 
 }  // namespace
@@ -185,23 +240,27 @@ cudaError_t launch_moe_sort(const int32_t *ids, int64_t N, int E, int align, int
                             int32_t *slot_of, int *fault, cudaStream_t s)
 {
     SortArgs a{ids, counts, offsets, row_of, slot_of, N, R, 0, E, align, fault};
-    // blocks: up to 2048 slots each (two of eight lookups a lane), 16 at most
+    // blocks: up to 2048 slots each, 16 at most
     int nb = 1;
     while (nb < 16 && int64_t(nb) * 2048 < N) nb *= 2;
-    const int64_t warps = int64_t(nb) * kSortWarps;
+    const int w = nb == 1 && N <= kFewWarps * 32 * kTile && E <= kFewWarps * 32 ? kFewWarps
+                                                                               : kSortWarps;
+    const int64_t warps = int64_t(nb) * w;
     a.seg = (N + warps * 32 - 1) / (warps * 32) * 32;
     const bool one = a.seg <= 32 * kTile;
-    void (*kernel)(SortArgs) = one ? k_moe_sort<true> : k_moe_sort<false>;
-    const size_t smem = (size_t(kSortWarps + 4) * E + 1) * sizeof(int);
+    void (*kernel)(SortArgs) = w == kFewWarps ? k_moe_sort<true, kFewWarps>
+                               : one          ? k_moe_sort<true, kSortWarps>
+                                              : k_moe_sort<false, kSortWarps>;
+    const size_t smem = sort_smem(E, one, w);
     cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kernel),
-                                   int((size_t(kSortWarps + 4) * kMoeMaxExperts + 1) * sizeof(int)));
+                                   int(sort_smem(32 * w, one, w)));
     if (e == cudaSuccess && nb > 8)
         e = cudaFuncSetAttribute(reinterpret_cast<const void *>(kernel),
                                  cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(nb));
-    cfg.blockDim = dim3(kSortThreads);
+    cfg.blockDim = dim3(unsigned(32 * w));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
