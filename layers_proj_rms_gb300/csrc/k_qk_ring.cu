@@ -104,7 +104,8 @@ struct Ring {
     }
     __device__ __forceinline__ void release() const
     {
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        // as tc::mbar_release: every lane's reads before the next copy's writes
+        asm volatile("fence.proxy.async.shared::cta;\nfence.acq_rel.cta;" ::: "memory");
         __syncwarp();
     }
     __device__ __forceinline__ void chunk(const char *head, int at_, bool on, Vec<T, 8> &v) const

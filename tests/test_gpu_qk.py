@@ -233,6 +233,14 @@ def test_a_token_does_not_depend_on_the_batch(M):
         assert torch.equal(x, y)
 
 
+def test_long_backward_repeats_bit_for_bit(M):
+    """The rings' slots are refilled while others are read."""
+    d = make(4096, 32, 8, 128, 128, torch.bfloat16, seed=9, P=4096)
+    first = run_bwd(M, d, False)
+    for _ in range(100):
+        assert all(torch.equal(x, y) for x, y in zip(run_bwd(M, d, False), first))
+
+
 def test_offsets_past_32_bits(M):
     """Token strides that put the last token more than 2^32 bytes away."""
     step, T, H, D = (1 << 30) + 64, 3, 2, 64
