@@ -149,11 +149,15 @@ __device__ __forceinline__ unsigned pack_of(float l, int e)
     return (key_of(l) & ~1023u) | unsigned(1023 - e);
 }
 
-// Exact choice by whole keys, one maximum at a time: lane j gets choice j.
-template <int NV, bool FULL>
-__device__ __noinline__ int choose_exact(const float (&l)[NV], int E, int k)
+// Exact choice by whole keys, one maximum at a time: lane j gets choice j.  The
+// row is loaded again: an array handed to a function would keep every row's
+// logits in local memory.
+template <class T, int NV, bool FULL>
+__device__ __noinline__ int choose_exact(const T *row, int E, int k)
 {
     const int lane = threadIdx.x & 31;
+    float l[NV];
+    load_row<T, NV, FULL>(row, E, lane, l);
     unsigned key[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = FULL || lane + 32 * i < E ? key_of(l[i]) : 0u;
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
         const unsigned next = __shfl_down_sync(kFull, mine, 1);
         const bool near = on && (mine ^ (lane == k - 1 ? last : next)) < 1024u;
         if (__any_sync(kFull, near && !(lane == k - 1 && rounds == k)))
-            my_id = choose_exact<NV, FULL>(l, E, k);
+            my_id = choose_exact<T, NV, FULL>(row, E, k);
     }
     const float my_l = on ? widen1(row[my_id]) : -INFINITY;
     float v;

@@ -64,20 +64,23 @@ __global__ void __launch_bounds__(kRowThreads)
     clear_padding(slot_of, R, chunks, xs);
 }
 
-// One 8-element chunk of one token per thread.
+// One 16-byte chunk (V elements) of one token per thread.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads)
     k_moe_combine(const T *__restrict__ ys, const float *__restrict__ w,
-                  const int32_t *__restrict__ row_of, int64_t n, int k, int64_t R, int64_t C8,
+                  const int32_t *__restrict__ row_of, int64_t n, int k, int64_t R, int64_t chunks,
                   T *__restrict__ f, int *fault)
 {
+    constexpr int V = 16 / int(sizeof(T));
     pdl_wait();
     const int64_t i = int64_t(blockIdx.x) * kRowThreads + threadIdx.x;
     if (i >= n) return;
-    const int64_t t = i / C8, q = i - t * C8;
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int64_t t = i / chunks, q = i - t * chunks;
+    float acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
     for (int j0 = 0; j0 < k; j0 += 8) {
-        Vec<T, 8> v[8];
+        Vec<T, V> v[8];
         float wj[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -87,21 +90,21 @@ __global__ void __launch_bounds__(kRowThreads)
                 const int64_t slot = t * k + j0 + j, r = plan_row(row_of, slot, R, fault);
                 if (r >= 0) {
                     wj[j] = w ? __ldg(w + slot) : 1.f;
-                    ld_vec(v[j], ys + (r * C8 + q) * 8);
+                    ld_vec(v[j], ys + (r * chunks + q) * V);
                 }
             }
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float y[8];
+            float y[V];
             widen(v[j], y);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = fmaf(wj[j], y[e], acc[e]);
+            for (int e = 0; e < V; ++e) acc[e] = fmaf(wj[j], y[e], acc[e]);
         }
     }
-    Vec<T, 8> o;
+    Vec<T, V> o;
     narrow(acc, o);
-    st_vec(f + i * 8, o);
+    st_vec(f + i * V, o);
 }
 
 // One token per block; the k sums of dw stay in registers over the row.
@@ -189,10 +192,11 @@ template <class T>
 cudaError_t combine_of(const void *ys, const float *w, const int32_t *row_of, int64_t tokens,
                        int k, int64_t R, int64_t C, void *f, int *fault, cudaStream_t s)
 {
-    const int64_t n = tokens * (C / 8), blocks = (n + kRowThreads - 1) / kRowThreads;
+    const int64_t chunks = C * int64_t(sizeof(T)) / 16, n = tokens * chunks;
+    const int64_t blocks = (n + kRowThreads - 1) / kRowThreads;
     MHC_PROF("k_moe_combine", s);
     return launch_k(k_moe_combine<T>, dim3(unsigned(blocks)), dim3(kRowThreads), 0, s,
-                    static_cast<const T *>(ys), w, row_of, n, k, R, C / 8, static_cast<T *>(f),
+                    static_cast<const T *>(ys), w, row_of, n, k, R, chunks, static_cast<T *>(f),
                     fault);
 }
 
