@@ -421,7 +421,8 @@ MHC_API mhc_status mhc_h_post_bda_compute_h_fwd(
 /* device error word (201 a position outside the table, 202 an expert   */
 /* outside [-1, E) in mhc_moe_sort, 203 a row outside [-1, R), 204 an   */
 /* expert outside [-1, E) in mhc_moe_router_bwd).                       */
-/* A token's results do not depend on T or on its place in the batch.   */
+/* A token's results do not depend on T or on its place in the batch;   */
+/* the batch-invariant and the bit-reproducible mode change nothing here.*/
 /* ------------------------------------------------------------------ */
 
 typedef enum { MHC_BF16 = 0, MHC_FP16 = 1, MHC_FP32 = 2 } mhc_dtype;
@@ -504,7 +505,10 @@ MHC_API int64_t mhc_moe_rows(int64_t T, int k, int E, int align);
  * offsets[E] the rows in use; row_of [T, k]: a slot's row, -1 if dropped;
  * slot_of [R]: a row's slot, -1 for padding and for the rows past
  * offsets[E].  mhc_moe_rows(T, k, E, align) <= R < 2^31.  T may be 0 (counts,
- * offsets and slot_of are still written). */
+ * offsets and slot_of are still written).
+ * The rows in use are known on the device alone, so the calls below work on
+ * all R rows; a caller that does know offsets[E] may hand them that many (and
+ * so spare the zeroing of the rest). */
 MHC_API mhc_status mhc_moe_sort(const int32_t *ids, int64_t T, int k, int E, int align,
                                 int64_t R, int32_t *counts, int32_t *offsets, int32_t *row_of,
                                 int32_t *slot_of, mhc_stream_t stream);

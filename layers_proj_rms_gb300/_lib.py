@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -510,21 +511,32 @@ def _heads(t, dtype, shape, name):
     return t.data_ptr(), st[:2]
 
 
-def _qk_shapes(q, k, cos, sin):
-    for t, name in ((q, "q"), (k, "k")):
-        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 3):
-            raise ValueError(f"{name} must be a [T, H, D] tensor")
-    one = q if q is not None else k
+def _qk_shapes(q, k, cos):
+    """dtype code and dtype, shapes of q and k, R and P."""
+    one = k if q is None else q
     if one is None:
         raise ValueError("q and k are both None")
-    code, dt = _act(one, "q" if q is not None else "k"), one.dtype
-    T, H, D = one.shape
-    sq = (T, H if q is not None else 0, D)
-    sk = (T, k.shape[1] if k is not None else 0, D)
+    code = _act(one, "k" if q is None else "q")
+    dt, shape = one.dtype, one.shape
+    if len(shape) != 3:
+        raise ValueError(f"{'k' if q is None else 'q'} must be a [T, H, D] tensor")
+    T, H, D = shape
+    sq = (T, 0, D) if q is None else (T, H, D)
+    sk = (T, 0, D)
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("k must be a [T, H, D] tensor")
+        sk = (T, k.shape[1], D)
     if cos is None:
         return code, dt, sq, sk, 0, 0
     P, half = cos.shape
     return code, dt, sq, sk, 2 * half, P
+
+
+@functools.lru_cache(maxsize=256)
+def _strides(*values):
+    """The C array of a call's strides (made once for the same values)."""
+    return (ctypes.c_int64 * len(values))(*values)
 
 
 def mhc_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, cos, sin, pos, eps, q_out, k_out,
@@ -532,14 +544,14 @@ def mhc_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, cos, sin, pos, eps, q_out, k_ou
     """q [T, Hq, D], k [T, Hk, D] and the outputs may be views with any token
     and head strides (slices of a packed qkv product, [H, T, D] layouts);
     q or k may be None; cos and sin None: no rotation."""
-    code, dt, sq, sk, R, P = _qk_shapes(q, k, cos, sin)
+    code, dt, sq, sk, R, P = _qk_shapes(q, k, cos)
     T, Hq, D = sq
     pq, a = _heads(q, dt, sq, "q")
     pk, b = _heads(k, dt, sk, "k")
     oq, c = _heads(q_out, dt, sq, "q_out")
     ok, d = _heads(k_out, dt, sk, "k_out")
     _ok(lib.mhc_qk_norm_rope_fwd(
-        pq, pk, code, _S8(*a, *b, *c, *d),
+        pq, pk, code, _strides(*a, *b, *c, *d),
         _ptr(gamma_q, _F32, (D,), "gamma_q"), _ptr(gamma_k, _F32, (D,), "gamma_k"),
         _ptr(cos, _F32, (P, R // 2), "cos"), _ptr(sin, _F32, (P, R // 2), "sin"),
         _ptr(pos, _I32, (T,), "pos"), T, Hq, sk[1], D, R, P, interleaved, eps, oq, ok,
@@ -548,7 +560,7 @@ def mhc_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, cos, sin, pos, eps, q_out, k_ou
 
 def mhc_qk_norm_rope_bwd(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, pos, eps, dq, dk,
                          dgamma_q=None, dgamma_k=None, ws=None, interleaved=False, stream=None):
-    code, dt, sq, sk, R, P = _qk_shapes(q, k, cos, sin)
+    code, dt, sq, sk, R, P = _qk_shapes(q, k, cos)
     T, Hq, D = sq
     pu, a = _heads(dq_out, dt, sq, "dq_out")
     pv, b = _heads(dk_out, dt, sk, "dk_out")
@@ -558,16 +570,12 @@ def mhc_qk_norm_rope_bwd(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, pos, 
     ok, f = _heads(dk, dt, sk, "dk")
     wp, wb = _ws(ws)
     _ok(lib.mhc_qk_norm_rope_bwd(
-        pu, pv, pq, pk, code, _S12(*a, *b, *c, *d, *e, *f),
+        pu, pv, pq, pk, code, _strides(*a, *b, *c, *d, *e, *f),
         _ptr(gamma_q, _F32, (D,), "gamma_q"), _ptr(gamma_k, _F32, (D,), "gamma_k"),
         _ptr(cos, _F32, (P, R // 2), "cos"), _ptr(sin, _F32, (P, R // 2), "sin"),
         _ptr(pos, _I32, (T,), "pos"), T, Hq, sk[1], D, R, P, interleaved, eps, oq, ok,
         _ptr(dgamma_q, _F32, (D,), "dgamma_q"), _ptr(dgamma_k, _F32, (D,), "dgamma_k"), wp, wb,
         _stream(stream)))
-
-
-_S8 = ctypes.c_int64 * 8
-_S12 = ctypes.c_int64 * 12
 
 
 def mhc_moe_router_fwd(logits, score, renorm, scale, ids, w, stream=None):

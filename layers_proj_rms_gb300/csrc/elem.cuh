@@ -43,6 +43,25 @@ __device__ __forceinline__ void ld_vec(Vec<T, V> &v, const T *p)
     }
 }
 
+// The same, kept in L1 for a second look.
+template <class T, int V>
+__device__ __forceinline__ void ld_vec_keep(Vec<T, V> &v, const T *p)
+{
+    constexpr int B = Vec<T, V>::kBytes;
+    if constexpr (B >= 16) {
+#pragma unroll
+        for (int i = 0; i < B / 16; ++i) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            v.w[4 * i] = u.x;
+            v.w[4 * i + 1] = u.y;
+            v.w[4 * i + 2] = u.z;
+            v.w[4 * i + 3] = u.w;
+        }
+    } else {
+        ld_vec(v, p);
+    }
+}
+
 template <class T, int V>
 __device__ __forceinline__ void st_vec(T *p, const Vec<T, V> &v)
 {

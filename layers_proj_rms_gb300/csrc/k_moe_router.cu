@@ -28,7 +28,9 @@ constexpr int kFaultChoice = 204;  // backward: an id outside [-1, E)
 
 namespace {
 
-constexpr int kRouterWarps = 4;  // 8: within 2%; 16: 20% slower
+// Warps of a block, and blocks per SM that the registers leave room for:
+// 16384 x 256 fp32, k = 8: 4, 12 take 8.3 us; 4, any 8.4; 8, 8 8.5; 16, any 10.6.
+constexpr int kRouterWarps = 4, kRouterPerSm = 12;
 
 __device__ __forceinline__ float warp_max(float v)
 {
@@ -86,7 +88,7 @@ __device__ __forceinline__ void load_row(const T *row, int E, int lane, float (&
         for (int i = 0; i < NV; i += RUN) {
             Vec<T, RUN> v;
             float f[RUN];
-            ld_vec(v, row + expert_of<NV, FULL>(lane, i));
+            ld_vec_keep(v, row + expert_of<NV, FULL>(lane, i));
             widen(v, f);
 #pragma unroll
             for (int e = 0; e < RUN; ++e) l[i + e] = f[e];
@@ -182,7 +184,7 @@ __device__ __noinline__ int choose_exact(const T *row, int E, int k)
 }
 
 template <class T, int NV, bool FULL>
-__global__ void __launch_bounds__(kRouterWarps * 32)
+__global__ void __launch_bounds__(kRouterWarps * 32, NV <= 8 ? kRouterPerSm : 1)
     k_moe_router(const T *__restrict__ logits, int64_t tokens, int E, int k, int score,
                  int renorm, float scale, int32_t *__restrict__ ids, float *__restrict__ w)
 {
