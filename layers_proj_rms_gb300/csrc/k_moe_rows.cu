@@ -6,10 +6,13 @@
 //   combine bwd:   dys[row] = w[t][j] df[t], padding rows 0;
 //                  dw[t][j] = sum_c df[t][c] ys[row][c], dropped slots 0
 //
-// All three are bound by HBM.  They walk over tokens, not over sorted rows: a
-// token's row is read once and its k rows are whole, contiguous 2C-byte rows
-// wherever they are, so every byte crosses HBM once.  Padding rows have no
-// token; each block clears those of its share of the sorted rows.
+// All three are bound by HBM (16384 x 4096, k = 4: dispatch 112 us, 97% of the
+// measured copy bandwidth, combine backward 193 us, 97%; 8192 x 7168, k = 8,
+// combine backward 365 us, 100%, once four blocks fit an SM: with two, 387).
+// They walk over tokens, not over sorted rows: a token's row is read once and
+// its k rows are whole, contiguous 2C-byte rows wherever they are, so every
+// byte crosses HBM once.  Padding rows have no token; each block clears those
+// of its share of the sorted rows.
 // Sums over j are in ascending j and sums over c in an order fixed by C
 // alone, so a token's results do not depend on T or on its place.
 #include "elem.cuh"
@@ -107,23 +110,27 @@ __global__ void __launch_bounds__(kRowThreads)
     st_vec(f + i * V, o);
 }
 
-// One token per block; the k sums of dw stay in registers over the row.
-template <class T>
-__global__ void __launch_bounds__(kRowThreads)
+// TPT threads of a block work on one token (32: a warp on its own, for rows of
+// up to 192 chunks; else the whole block); the sums of dw of KM slots stay in
+// registers over the row.
+template <class T, int TPT, int KM>
+__global__ void __launch_bounds__(kRowThreads, TPT == 32 && KM == 8 ? 3 : 4)
     k_moe_combine_bwd(const T *__restrict__ df, const T *__restrict__ ys,
                       const float *__restrict__ w, const int32_t *__restrict__ row_of,
-                      const int32_t *__restrict__ slot_of, int64_t T_, int k, int64_t R,
-                      int64_t C8, T *__restrict__ dys, float *__restrict__ dw, int *fault)
+                      const int32_t *__restrict__ slot_of, int64_t tokens, int k, int64_t R,
+                      int64_t chunks, T *__restrict__ dys, float *__restrict__ dw, int *fault)
 {
-    __shared__ float red[8][kRowThreads / 32];
+    constexpr int V = 16 / int(sizeof(T)), PER = kRowThreads / TPT;
+    __shared__ float red[KM][kRowThreads / 32];
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int64_t t = blockIdx.x; t < T_; t += gridDim.x)
-        for (int j0 = 0; j0 < k; j0 += 8) {
-            int64_t row[8];
-            float wj[8], acc[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, me = threadIdx.x % TPT;
+    const int64_t step = int64_t(gridDim.x) * PER;
+    for (int64_t t = int64_t(blockIdx.x) * PER + threadIdx.x / TPT; t < tokens; t += step)
+        for (int j0 = 0; j0 < k; j0 += KM) {
+            int64_t row[KM];
+            float wj[KM], acc[KM];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < KM; ++j) {
                 acc[j] = wj[j] = 0.f;
                 row[j] = -1;
                 if (j0 + j < k) {
@@ -132,47 +139,55 @@ __global__ void __launch_bounds__(kRowThreads)
                     if (row[j] >= 0) wj[j] = w ? __ldg(w + slot) : 1.f;
                 }
             }
-            for (int64_t q = threadIdx.x; q < C8; q += blockDim.x) {
-                Vec<T, 8> dv, yv[8];
-                ld_vec(dv, df + (t * C8 + q) * 8);
+            for (int64_t q = me; q < chunks; q += TPT) {
+                Vec<T, V> dv, yv[KM];
+                ld_vec(dv, df + (t * chunks + q) * V);
                 if (dw)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (row[j] >= 0) ld_vec(yv[j], ys + (row[j] * C8 + q) * 8);
-                float d[8];
+                    for (int j = 0; j < KM; ++j)
+                        if (row[j] >= 0) ld_vec(yv[j], ys + (row[j] * chunks + q) * V);
+                float d[V];
                 widen(dv, d);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
+                for (int j = 0; j < KM; ++j)
                     if (row[j] >= 0) {
-                        float o[8];
+                        float o[V];
                         if (dw) {
-                            float y[8];
+                            float y[V];
                             widen(yv[j], y);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) acc[j] = fmaf(d[e], y[e], acc[j]);
+                            for (int e = 0; e < V; ++e) acc[j] = fmaf(d[e], y[e], acc[j]);
                         }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = wj[j] * d[e];
-                        Vec<T, 8> ov;
+                        for (int e = 0; e < V; ++e) o[e] = wj[j] * d[e];
+                        Vec<T, V> ov;
                         narrow(o, ov);
-                        st_vec(dys + (row[j] * C8 + q) * 8, ov);
+                        st_vec(dys + (row[j] * chunks + q) * V, ov);
                     }
             }
             if (!dw) continue;
+            if constexpr (TPT == 32) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float s = warp_sum(acc[j]);
-                if (lane == 0) red[j][warp] = s;
+                for (int j = 0; j < KM; ++j) {
+                    const float s = warp_sum(acc[j]);
+                    if (lane == j && j0 + j < k) dw[t * k + j0 + j] = s;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < KM; ++j) {
+                    const float s = warp_sum(acc[j]);
+                    if (lane == 0) red[j][warp] = s;
+                }
+                __syncthreads();
+                if (threadIdx.x < KM && j0 + int(threadIdx.x) < k) {
+                    float s = 0.f;
+                    for (int i = 0; i < TPT / 32; ++i) s += red[threadIdx.x][i];
+                    dw[t * k + j0 + threadIdx.x] = s;
+                }
+                __syncthreads();
             }
-            __syncthreads();
-            if (threadIdx.x < 8 && j0 + int(threadIdx.x) < k) {
-                float s = 0.f;
-                for (int i = 0; i < int(blockDim.x >> 5); ++i) s += red[threadIdx.x][i];
-                dw[t * k + j0 + threadIdx.x] = s;
-            }
-            __syncthreads();
         }
-    clear_padding(slot_of, R, C8 * int64_t(sizeof(T)) / 2, reinterpret_cast<uint4 *>(dys));
+    clear_padding(slot_of, R, chunks, reinterpret_cast<uint4 *>(dys));
 }
 
 // A block per token, and no more than eight sorted rows to look over for each.
@@ -205,10 +220,18 @@ cudaError_t combine_bwd_of(const void *df, const void *ys, const float *w, const
                            const int32_t *slot_of, int64_t tokens, int k, int64_t R, int64_t C,
                            void *dys, float *dw, int *fault, cudaStream_t s)
 {
+    const int64_t chunks = C * int64_t(sizeof(T)) / 16;
+    // a block on one token, or a warp: rows of 166 chunks, k = 5, 30.5 and 24.0 us
+    // (3311 tokens); of 256 chunks, k = 6, 44.9 and 47.4 (4096 tokens).  The rule
+    // looks at C alone, as the order of dw's sums goes by it.
+    const bool one = chunks > 192;
+    const int64_t per = one ? 1 : kRowThreads / 32, need = (tokens + per - 1) / per;
     MHC_PROF("k_moe_combine_bwd", s);
-    return launch_k(k_moe_combine_bwd<T>, dim3(row_blocks(tokens, R)), dim3(row_threads(C / 8)), 0,
-                    s, static_cast<const T *>(df), static_cast<const T *>(ys), w, row_of, slot_of,
-                    tokens, k, R, C / 8, static_cast<T *>(dys), dw, fault);
+    auto kernel = k <= 4 ? (one ? k_moe_combine_bwd<T, kRowThreads, 4> : k_moe_combine_bwd<T, 32, 4>)
+                         : (one ? k_moe_combine_bwd<T, kRowThreads, 8> : k_moe_combine_bwd<T, 32, 8>);
+    return launch_k(kernel, dim3(row_blocks(need, R)), dim3(kRowThreads), 0, s, static_cast<const T *>(df),
+                    static_cast<const T *>(ys), w, row_of, slot_of, tokens, k, R, chunks,
+                    static_cast<T *>(dys), dw, fault);
 }
 
 }  // namespace

@@ -44,19 +44,20 @@ struct SortArgs {
     int *fault;
 };
 
-// ids of one tile of a warp's segment: kTile x 32 slots from b on
-constexpr int kTile = 8;
+// ids of one tile of a warp's segment: TILE x 32 slots from b on
+constexpr int kTile = 8;  // at most
 
+template <int TILE>
 __device__ __forceinline__ void load_tile(const SortArgs &A, int64_t b, int64_t s1, int lane,
-                                          int (&e)[kTile])
+                                          int (&e)[TILE])
 {
 #pragma unroll
-    for (int q = 0; q < kTile; ++q) {
+    for (int q = 0; q < TILE; ++q) {
         const int64_t i = b + 32 * q + lane;
         e[q] = i < s1 ? __ldg(A.ids + i) : -1;
     }
 #pragma unroll
-    for (int q = 0; q < kTile; ++q)
+    for (int q = 0; q < TILE; ++q)
         if (e[q] < -1 || e[q] >= A.E) {
             report_fault(A.fault, kFaultExpert);
             e[q] = -1;
@@ -74,24 +75,27 @@ __device__ __forceinline__ unsigned bit_mask(int e, int b)
 // Ranks of a tile's slots among the segment's slots of the same expert; mine
 // holds how many there were before, and is brought up to date.  The lanes of
 // equal ids are found by a ballot per bit of the id.
-__device__ __forceinline__ void rank_tile(const int (&e)[kTile], int bits, int *mine, int lane,
-                                          int (&rank)[kTile])
+template <int TILE>
+__device__ __forceinline__ void rank_tile(const int (&e)[TILE], int bits, int *mine, int lane,
+                                          int (&rank)[TILE])
 {
     const unsigned below = (1u << lane) - 1u;
-    unsigned same[kTile];
+    unsigned same[TILE];
 #pragma unroll
-    for (int q = 0; q < kTile; ++q) same[q] = __ballot_sync(kFull, e[q] >= 0);  // -1: not used
+    for (int q = 0; q < TILE; ++q) {
+        same[q] = __ballot_sync(kFull, e[q] >= 0);  // a dropped slot's is not used
+    }
 #pragma unroll
     for (int b = 0; b < 10; ++b) {  // E <= 1024
         if (b >= bits) break;
 #pragma unroll
-        for (int q = 0; q < kTile; ++q) {
+        for (int q = 0; q < TILE; ++q) {
             const unsigned m = __ballot_sync(kFull, e[q] & (1 << b));
             same[q] &= ~(m ^ bit_mask(e[q], b));
         }
     }
 #pragma unroll
-    for (int q = 0; q < kTile; ++q) {
+    for (int q = 0; q < TILE; ++q) {
         rank[q] = e[q] >= 0 ? mine[e[q]] + __popc(same[q] & below) : 0;
         __syncwarp();
         if (e[q] >= 0 && (same[q] & below) == 0) mine[e[q]] += __popc(same[q]);
@@ -99,8 +103,16 @@ __device__ __forceinline__ void rank_tile(const int (&e)[kTile], int bits, int *
     }
 }
 
-// ONE: every segment is one tile.  W: warps of a block; E <= 32 W
-template <bool ONE, int W>
+// slot_of = -1 everywhere: thread i of n
+__device__ __forceinline__ void fill_unused(int32_t *slot_of, int64_t R, int64_t i, int64_t n)
+{
+    const int4 none = make_int4(-1, -1, -1, -1);
+    for (int64_t r = i; r < R / 4; r += n) reinterpret_cast<int4 *>(slot_of)[r] = none;
+    if (i < R % 4) slot_of[R / 4 * 4 + i] = -1;
+}
+
+// ONE: every segment is one tile (of TILE x 32 slots).  W: warps of a block; E <= 32 W
+template <bool ONE, int W, int TILE>
 __global__ void __launch_bounds__(32 * W) k_moe_sort(const SortArgs A)
 {
     extern __shared__ int sm[];
@@ -111,7 +123,7 @@ __global__ void __launch_bounds__(32 * W) k_moe_sort(const SortArgs A)
     int *off = base + E;                  // [E + 1] padded offsets
     int *count = off + E + 1;             // [E] counts over all blocks
     int *loc = count + E;                 // [E] this block's slots of lower experts
-    int *sorted = loc + E;                // [32 W kTile] ONE: the block's slots by expert
+    int *sorted = loc + E;                // [32 W TILE] ONE: the block's slots by expert
     __shared__ int wsum[2][W];
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -125,9 +137,13 @@ __global__ void __launch_bounds__(32 * W) k_moe_sort(const SortArgs A)
     pdl_wait();
 
     const int bits = 32 - __clz(E - 1);  // of an id; 0 where E = 1
-    int e[kTile], rk[kTile];
-    for (int64_t b = s0; b < s1; b += 32 * kTile) {
-        load_tile(A, b, s1, lane, e);
+    int e[TILE], rk[TILE];
+    if (ONE) load_tile(A, s0, s1, lane, e);
+    // first -1 everywhere (the slots' rows follow after the cluster's barriers):
+    // on few slots this takes 0.3 to 1.4 us less than clearing the padding alone
+    if (ONE) fill_unused(A.slot_of, A.R, int64_t(rank) * (32 * W) + tid, int64_t(nb) * (32 * W));
+    for (int64_t b = s0; b < s1; b += 32 * TILE) {
+        if (!ONE) load_tile(A, b, s1, lane, e);
         rank_tile(e, bits, mine, lane, rk);
     }
     __syncthreads();
@@ -174,8 +190,8 @@ __global__ void __launch_bounds__(32 * W) k_moe_sort(const SortArgs A)
         off[tid] = start;
         base[tid] = start + before;
         count[tid] = all;
-        loc[tid] = mine_from;
         if (tid == E - 1) off[E] = start + padded;
+        loc[tid] = mine_from;
         if (rank == 0) {
             A.counts[tid] = all;
             A.offsets[tid] = start;
@@ -191,7 +207,7 @@ __global__ void __launch_bounds__(32 * W) k_moe_sort(const SortArgs A)
         // 32 lanes to a line of its own, they took 5 us of 131072 slots' 14.6)
         const int64_t block0 = int64_t(rank) * W * A.seg;
 #pragma unroll
-        for (int q = 0; q < kTile; ++q) {
+        for (int q = 0; q < TILE; ++q) {
             const int64_t i = s0 + 32 * q + lane;
             if (i < s1) {
                 const int x = e[q], r = x < 0 ? 0 : mine[x] + rk[q];
@@ -206,11 +222,11 @@ __global__ void __launch_bounds__(32 * W) k_moe_sort(const SortArgs A)
             A.slot_of[base[x] + i - loc[x]] = int(block0) + (sorted[i] >> 10);
         }
     } else {
-        for (int64_t b = s0; b < s1; b += 32 * kTile) {
+        for (int64_t b = s0; b < s1; b += 32 * TILE) {
             load_tile(A, b, s1, lane, e);
             rank_tile(e, bits, mine, lane, rk);
 #pragma unroll
-            for (int q = 0; q < kTile; ++q) {
+            for (int q = 0; q < TILE; ++q) {
                 const int64_t i = b + 32 * q + lane;
                 if (i < s1) {
                     const int row = e[q] < 0 ? -1 : base[e[q]] + rk[q];
@@ -220,12 +236,15 @@ __global__ void __launch_bounds__(32 * W) k_moe_sort(const SortArgs A)
             }
         }
     }
-    // padding of the segments, then the rows past the last one
-    for (int e = int(gw); e < E; e += nb * W)
-        for (int r = off[e] + count[e] + lane; r < off[e + 1]; r += 32) A.slot_of[r] = -1;
-    for (int64_t r = off[E] + int64_t(rank) * (32 * W) + tid; r < A.R;
-         r += int64_t(nb) * (32 * W))
-        A.slot_of[r] = -1;
+    if constexpr (!ONE) {
+        // padding of the segments, eight lanes to an expert, then the rows past
+        // the last one
+        for (int x = int(gw * 4) + lane / 8; x < E; x += nb * W * 4)
+            for (int r = off[x] + count[x] + lane % 8; r < off[x + 1]; r += 8) A.slot_of[r] = -1;
+        for (int64_t r = off[E] + int64_t(rank) * (32 * W) + tid; r < A.R;
+             r += int64_t(nb) * (32 * W))
+            A.slot_of[r] = -1;
+    }
 }
 
 size_t sort_smem(int E, bool one, int warps)
@@ -240,17 +259,22 @@ cudaError_t launch_moe_sort(const int32_t *ids, int64_t N, int E, int align, int
                             int32_t *slot_of, int *fault, cudaStream_t s)
 {
     SortArgs a{ids, counts, offsets, row_of, slot_of, N, R, 0, E, align, fault};
-    // blocks: up to 2048 slots each, 16 at most
+    // blocks: up to 1024 slots each (4096 slots: 6.2 us; up to 4096 each: 8.2), 16
+    // at most
     int nb = 1;
-    while (nb < 16 && int64_t(nb) * 2048 < N) nb *= 2;
+    while (nb < 16 && int64_t(nb) * 1024 < N) nb *= 2;
     const int w = nb == 1 && N <= kFewWarps * 32 * kTile && E <= kFewWarps * 32 ? kFewWarps
                                                                                : kSortWarps;
     const int64_t warps = int64_t(nb) * w;
     a.seg = (N + warps * 32 - 1) / (warps * 32) * 32;
     const bool one = a.seg <= 32 * kTile;
-    void (*kernel)(SortArgs) = w == kFewWarps ? k_moe_sort<true, kFewWarps>
-                               : one          ? k_moe_sort<true, kSortWarps>
-                                              : k_moe_sort<false, kSortWarps>;
+    void (*kernel)(SortArgs) = a.seg <= 32    ? k_moe_sort<true, kSortWarps, 1>
+                               : a.seg <= 64  ? k_moe_sort<true, kSortWarps, 2>
+                               : a.seg <= 128 ? k_moe_sort<true, kSortWarps, 4>
+                               : one          ? k_moe_sort<true, kSortWarps, kTile>
+                                              : k_moe_sort<false, kSortWarps, kTile>;
+    if (w == kFewWarps)
+        kernel = a.seg <= 32 ? k_moe_sort<true, kFewWarps, 1> : k_moe_sort<true, kFewWarps, kTile>;
     const size_t smem = sort_smem(E, one, w);
     cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kernel),
                                    int(sort_smem(32 * w, one, w)));

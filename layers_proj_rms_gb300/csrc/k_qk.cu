@@ -18,7 +18,7 @@
 //
 // V = 8 (16-byte vectors for 16-bit types) needs R a multiple of 16, D of 8,
 // and strides and pointers on 16 bytes; V = 2 needs R a multiple of 4 and D
-// of 2; V = 1 takes anything.  A lane of a head has K units (V = 8: one).  The
+// of 2; V = 1 takes anything (V = 4 was no faster than V = 2).  A lane of a head has K units (V = 8: one).  The
 // order of a head's sums is fixed by V, D and R: it depends neither on the
 // grid nor on T.
 //
@@ -52,8 +52,9 @@ __device__ __forceinline__ void zero_token(const QkTensor &m, int64_t t, int h0,
     }
 }
 
-// MINB: blocks per SM that the registers must leave room for.
-template <class T, int V, int K, int HPI, bool INTER, int MINB, int FLG>
+// MINB: blocks per SM that the registers must leave room for.  ALL: every unit is
+// rotated (R = D).
+template <class T, int V, int K, int HPI, bool INTER, int MINB, int FLG, bool ALL>
 __global__ void __launch_bounds__(kQkWarps * 32, MINB)
     k_qk_fwd(const __grid_constant__ QkArgs A, const __grid_constant__ QkGeom ge)
 {
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, MINB)
             E ga[N], gb[N];
             gamma_e<V>(gam + (va[q] ? at[q] : 0), ga);
             gamma_e<V>(gam + (vb[q] ? bt[q] : 0), gb);
-            if (FLG >= 0 || l + q * G < hr) {
+            if (ALL || l + q * G < hr) {
                 Rope<V, INTER> r;
                 r.load(A.cs, A.sn, p * half + V * (l + q * G));
                 f[q].fold(ga, gb, r);
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, MINB)
 #pragma unroll
             for (int q = 0; q < K; ++q) {
                 E ya[N], yb[N];
-                f[q].apply(a[q], b[q], rho, FLG >= 0 || l + q * G < hr, ya, yb);
+                f[q].apply(a[q], b[q], rho, ALL || l + q * G < hr, ya, yb);
                 Vec<T, V> o;
                 narrow_e<T, V>(ya, o);
                 if (va[q]) st_vec(row + at[q], o);
@@ -307,7 +308,7 @@ int qk_vec(const QkArgs &a, int es)
 {
     for (int v : {8, 2}) {
         bool ok = a.D % v == 0 && (a.R / 2) % v == 0;
-        const int bytes = v == 8 ? 16 : 2 * es;
+        const int bytes = v * es < 16 ? v * es : 16;
         for (const QkTensor &m : a.m)
             if (m.H > 0)
                 ok = ok && on(m.x, m.x_t, m.x_h, es, bytes) && on(m.out, m.out_t, m.out_h, es, bytes) &&
@@ -329,14 +330,14 @@ cudaError_t sum_dgamma(const QkArgs &a, const float *part, int blocks, cudaStrea
                     a.D, a.m[0].dgamma, a.m[1].dgamma);
 }
 
-template <class T, int V, int K, int HPI, int MINB, int FLG = -1>
+template <class T, int V, int K, int HPI, int MINB, int FLG = -1, bool ALL = false>
 cudaError_t run_fwd(const QkArgs &a, cudaStream_t s)
 {
     int blocks;
     const QkGeom g = qk_geom(a, V, K, HPI, qk_blocks(MINB), &blocks);
     const size_t smem = size_t(2) * ((a.D + 7) & ~7) * sizeof(float);
-    auto kernel = V > 1 && a.interleaved ? k_qk_fwd<T, V, K, HPI, (V > 1), MINB, FLG>
-                                         : k_qk_fwd<T, V, K, HPI, false, MINB, FLG>;
+    auto kernel = V > 1 && a.interleaved ? k_qk_fwd<T, V, K, HPI, (V > 1), MINB, FLG, ALL>
+                                         : k_qk_fwd<T, V, K, HPI, false, MINB, FLG, ALL>;
     MHC_PROF("k_qk_fwd", s);
     return launch_k(kernel, dim3(unsigned(blocks)), dim3(kQkWarps * 32), smem, s, a, g);
 }
@@ -377,11 +378,15 @@ cudaError_t fwd_of(const QkArgs &a, cudaStream_t s)
     switch (qk_vec(a, int(sizeof(T)))) {
     case 8:
         if (!qk_many(a)) return run_fwd<T, 8, 1, 1, 3>(a, s);
-        if constexpr (sizeof(T) == 2) switch (a.R == a.D ? a.D : 0) {
-            case 64: return run_fwd<T, 8, 1, kFwdHeads, kFwdPerSm, 2>(a, s);
-            case 128: return run_fwd<T, 8, 1, kFwdHeads, kFwdPerSm, 3>(a, s);
-            case 256: return run_fwd<T, 8, 1, kFwdHeads, kFwdPerSm, 4>(a, s);
+        if constexpr (sizeof(T) == 2) {
+            constexpr int h = kFwdHeads, b = kFwdPerSm;
+            const bool all = a.R == a.D;
+            switch (a.D) {
+            case 64: return all ? run_fwd<T, 8, 1, h, b, 2, true>(a, s) : run_fwd<T, 8, 1, h, b, 2>(a, s);
+            case 128: return all ? run_fwd<T, 8, 1, h, b, 3, true>(a, s) : run_fwd<T, 8, 1, h, b, 3>(a, s);
+            case 256: return all ? run_fwd<T, 8, 1, h, b, 4, true>(a, s) : run_fwd<T, 8, 1, h, b, 4>(a, s);
             }
+        }
         return run_fwd<T, 8, 1, kFwdHeads, kFwdPerSm>(a, s);
     case 2:
         if (a.D <= 64) return run_fwd<T, 2, 2, kNarrowHeads, kNarrowPerSm>(a, s);

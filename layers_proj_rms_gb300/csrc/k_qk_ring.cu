@@ -31,8 +31,8 @@ struct RingGeom {
 };
 
 // A warp's life: which heads, where its ring is, and the copies into it.
-// FLG >= 0: a head is exactly 2^FLG lanes' units and all of it is rotated.
-template <class T, int HPI, int FLG, int S>
+// FLG >= 0: a head is exactly 2^FLG lanes' units; ALL: and R = D.
+template <class T, int HPI, int FLG, bool ALL, int S>
 struct Ring {
     const QkArgs &A;
     const QkTensor &m;
@@ -62,7 +62,7 @@ struct Ring {
         }
         __syncwarp();
     }
-    __device__ __forceinline__ bool turned() const { return FLG >= 0 || l < hr; }
+    __device__ __forceinline__ bool turned() const { return ALL || l < hr; }
     __device__ __forceinline__ bool known(int p) const { return A.R == 0 || (p >= 0 && p < A.P); }
     // the position of token t (past the last one: any); P is below 2^31 when
     // there are positions, and T <= P when there are none
@@ -185,7 +185,7 @@ struct Ring {
 };
 
 // dgp: [gridDim.x][2][D] partial sums of dgamma, one row per block.
-template <class T, int HPI, bool INTER, int FLG, int S, int MINB>
+template <class T, int HPI, bool INTER, int FLG, bool ALL, int S, int MINB>
 __global__ void __launch_bounds__(kQkWarps * 32, MINB)
     k_qk_ring_bwd(const __grid_constant__ QkArgs A, const __grid_constant__ RingGeom ge,
                   float *__restrict__ dgp)
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kQkWarps * 32, MINB)
     char *rings = reinterpret_cast<char *>(sm + 2 * gamma_row(A.D));
     if ((threadIdx.x & 31) == 0) owner[warp] = active ? w.which : -1;
     if (active) {
-        const Ring<T, HPI, FLG, S> r(A, ge, w, rings + warp * S * ge.slot, bar[warp]);
+        const Ring<T, HPI, FLG, ALL, S> r(A, ge, w, rings + warp * S * ge.slot, bar[warp]);
         const float *gam = sm + (w.which ? gamma_row(A.D) : 0);
         const float inv_d = 1.f / float(A.D);
         const int64_t out_h = r.m.out_h;
@@ -279,7 +279,7 @@ size_t ring_smem(const QkArgs &a, int slot, int slots)
     return size_t(2) * ((a.D + 7) & ~7) * sizeof(float) + size_t(kQkWarps) * slots * slot;
 }
 
-template <class T, int HPI, int S, int MINB, int FLG>
+template <class T, int HPI, int S, int MINB, int FLG = -1, bool ALL = false>
 cudaError_t run_bwd(const QkArgs &a, float *part, int *blocks, cudaStream_t s)
 {
     static_assert(qk_blocks(MINB) <= kQkBwdMaxBlocks, "the workspace has a row per block");
@@ -287,8 +287,8 @@ cudaError_t run_bwd(const QkArgs &a, float *part, int *blocks, cudaStream_t s)
     g.w = qk_geom(a, 8, 1, HPI, qk_blocks(MINB), blocks);
     g.slot = slot_bytes(a, sizeof(T), g.w.lg, HPI, S);
     const size_t smem = ring_smem(a, g.slot, S);
-    auto kernel = a.interleaved ? k_qk_ring_bwd<T, HPI, true, FLG, S, MINB>
-                                : k_qk_ring_bwd<T, HPI, false, FLG, S, MINB>;
+    auto kernel = a.interleaved ? k_qk_ring_bwd<T, HPI, true, FLG, ALL, S, MINB>
+                                : k_qk_ring_bwd<T, HPI, false, FLG, ALL, S, MINB>;
     const cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kernel), int(smem));
     if (e != cudaSuccess) return e;
     MHC_PROF("k_qk_ring_bwd", s);
@@ -301,12 +301,22 @@ template <class T>
 cudaError_t qk_ring_bwd(const QkArgs &a, float *part, int *blocks, cudaStream_t s)
 {
     constexpr int heads = sizeof(T) == 4 ? kHeads / 2 : kHeads;  // as many bytes
-    if constexpr (sizeof(T) == 2) switch (a.R == a.D ? a.D : 0) {
-        case 64: return run_bwd<T, heads, kSlots, kPerSm, 2>(a, part, blocks, s);
-        case 128: return run_bwd<T, heads, kSlots, kPerSm, 3>(a, part, blocks, s);
-        case 256: return run_bwd<T, heads, kSlots, kPerSm, 4>(a, part, blocks, s);
+    if constexpr (sizeof(T) == 2) {
+        constexpr int h = heads, n = kSlots, b = kPerSm;
+        const bool all = a.R == a.D;
+        switch (a.D) {
+        case 64:
+            return all ? run_bwd<T, h, n, b, 2, true>(a, part, blocks, s)
+                       : run_bwd<T, h, n, b, 2>(a, part, blocks, s);
+        case 128:
+            return all ? run_bwd<T, h, n, b, 3, true>(a, part, blocks, s)
+                       : run_bwd<T, h, n, b, 3>(a, part, blocks, s);
+        case 256:
+            return all ? run_bwd<T, h, n, b, 4, true>(a, part, blocks, s)
+                       : run_bwd<T, h, n, b, 4>(a, part, blocks, s);
         }
-    return run_bwd<T, heads, kSlots, kPerSm, -1>(a, part, blocks, s);
+    }
+    return run_bwd<T, heads, kSlots, kPerSm>(a, part, blocks, s);
 }
 
 template cudaError_t qk_ring_bwd<bf16>(const QkArgs &, float *, int *, cudaStream_t);

@@ -48,9 +48,9 @@ __device__ __forceinline__ void unit_at(int u, int hr, int half, bool inter, int
 template <int V, bool SHARED>
 __device__ __forceinline__ void load_f(const float *p, float (&f)[V])
 {
-    if constexpr (V == 8) {
+    if constexpr (V >= 4) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < V / 4; ++q) {
             const float4 *g = reinterpret_cast<const float4 *>(p) + q;
             const float4 v = SHARED ? *g : __ldg(g);
             f[4 * q] = v.x; f[4 * q + 1] = v.y; f[4 * q + 2] = v.z; f[4 * q + 3] = v.w;
