@@ -122,7 +122,9 @@ def random_ids(T, k, E, kind, seed=0):
 @pytest.mark.parametrize("kind", ["skewed", "one", "none"])
 @pytest.mark.parametrize("T,k,E,align", [(0, 2, 5, 8), (1, 1, 1, 1), (1, 8, 256, 16), (37, 4, 60, 16),
                                          (511, 2, 7, 1), (1000, 32, 1024, 128), (4097, 8, 61, 64),
-                                         (20011, 8, 256, 128), (3, 3, 1000, 65536)])
+                                         (20011, 8, 256, 128), (3, 3, 1000, 65536),
+                                         (2000, 32, 1024, 8), (8192, 4, 33, 16), (32769, 1, 2, 4),
+                                         (70001, 5, 64, 32)])
 def test_sort(M, T, k, E, align, kind):
     ids = random_ids(T, k, E, kind)
     want_rows = M.mhc_moe_rows(T, k, E, align)
