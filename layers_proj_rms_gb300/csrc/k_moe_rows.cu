@@ -67,26 +67,22 @@ __global__ void __launch_bounds__(kRowThreads)
     clear_padding(slot_of, R, chunks, xs);
 }
 
-// One 16-byte chunk (V elements) of one token per thread.
-template <class T>
-__global__ void __launch_bounds__(kRowThreads)
-    k_moe_combine(const T *__restrict__ ys, const float *__restrict__ w,
-                  const int32_t *__restrict__ row_of, int64_t n, int k, int64_t R, int64_t chunks,
-                  T *__restrict__ f, int *fault)
+// sum_j w[t][j] ys[row][chunk q] for one token's chunk of V elements; KM rows
+// at a time are on their way.
+template <class T, int KM>
+__device__ __forceinline__ void combine_chunk(const T *ys, const float *w, const int32_t *row_of,
+                                              int64_t t, int64_t q, int k, int64_t R,
+                                              int64_t chunks, T *f, int *fault)
 {
     constexpr int V = 16 / int(sizeof(T));
-    pdl_wait();
-    const int64_t i = int64_t(blockIdx.x) * kRowThreads + threadIdx.x;
-    if (i >= n) return;
-    const int64_t t = i / chunks, q = i - t * chunks;
     float acc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    for (int j0 = 0; j0 < k; j0 += 8) {
-        Vec<T, V> v[8];
-        float wj[8];
+    for (int j0 = 0; j0 < k; j0 += KM) {
+        Vec<T, V> v[KM];
+        float wj[KM];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < KM; ++j) {
             wj[j] = 0.f;
             zero_vec(v[j]);
             if (j0 + j < k) {
@@ -98,7 +94,7 @@ __global__ void __launch_bounds__(kRowThreads)
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < KM; ++j) {
             float y[V];
             widen(v[j], y);
 #pragma unroll
@@ -107,7 +103,28 @@ __global__ void __launch_bounds__(kRowThreads)
     }
     Vec<T, V> o;
     narrow(acc, o);
-    st_vec(f + i * V, o);
+    st_vec(f + (t * chunks + q) * V, o);
+}
+
+// BLOCK: a block on one token at a time (its rows are looked up once for all
+// chunks); else one chunk of one token per thread (for few tokens, short rows).
+template <class T, bool BLOCK, int KM>
+__global__ void __launch_bounds__(kRowThreads)
+    k_moe_combine(const T *__restrict__ ys, const float *__restrict__ w,
+                  const int32_t *__restrict__ row_of, int64_t tokens, int k, int64_t R,
+                  int64_t chunks, T *__restrict__ f, int *fault)
+{
+    pdl_wait();
+    if constexpr (BLOCK) {
+        for (int64_t t = blockIdx.x; t < tokens; t += gridDim.x)
+            for (int64_t q = threadIdx.x; q < chunks; q += kRowThreads)
+                combine_chunk<T, KM>(ys, w, row_of, t, q, k, R, chunks, f, fault);
+    } else {
+        const int64_t i = int64_t(blockIdx.x) * kRowThreads + threadIdx.x;
+        if (i >= tokens * chunks) return;
+        const int64_t t = i / chunks;
+        combine_chunk<T, KM>(ys, w, row_of, t, i - t * chunks, k, R, chunks, f, fault);
+    }
 }
 
 // TPT threads of a block work on one token (32: a warp on its own, for rows of
@@ -207,12 +224,18 @@ template <class T>
 cudaError_t combine_of(const void *ys, const float *w, const int32_t *row_of, int64_t tokens,
                        int k, int64_t R, int64_t C, void *f, int *fault, cudaStream_t s)
 {
-    const int64_t chunks = C * int64_t(sizeof(T)) / 16, n = tokens * chunks;
-    const int64_t blocks = (n + kRowThreads - 1) / kRowThreads;
+    const int64_t chunks = C * int64_t(sizeof(T)) / 16;
+    // 1001 tokens of 1792 chunks, k = 6: a block a token 29.6 us, a chunk a thread
+    // 31.5; 16384 of 512, k = 4: 105 and 116; 12598 of 305, k = 7: 83 and 79.  A
+    // chunk's sum is the same either way.
+    const bool block = chunks >= 512 && tokens >= kSplitSms * 4;
+    const int64_t blocks = block ? row_blocks(tokens, 0)
+                                 : (tokens * chunks + kRowThreads - 1) / kRowThreads;
     MHC_PROF("k_moe_combine", s);
-    return launch_k(k_moe_combine<T>, dim3(unsigned(blocks)), dim3(kRowThreads), 0, s,
-                    static_cast<const T *>(ys), w, row_of, n, k, R, chunks, static_cast<T *>(f),
-                    fault);
+    auto kernel = k <= 4 ? (block ? k_moe_combine<T, true, 4> : k_moe_combine<T, false, 4>)
+                         : (block ? k_moe_combine<T, true, 8> : k_moe_combine<T, false, 8>);
+    return launch_k(kernel, dim3(unsigned(blocks)), dim3(kRowThreads), 0, s, static_cast<const T *>(ys), w,
+                    row_of, tokens, k, R, chunks, static_cast<T *>(f), fault);
 }
 
 template <class T>
