@@ -36,7 +36,8 @@
  *    4 or 8; 0 <= iters <= 64.  The ops that take W (they run on the tensor
  *    cores with 32-bit TMA coordinates) need T < 2^31 and n*C < 2^31.
  *  - T (or M, rows) may be 0: the call then returns MHC_OK and does nothing.
- *  - Results are deterministic: no atomics, fixed reduction order; the same
+ *  - Results are deterministic: fixed reduction order, no atomics (but counts
+ *    of whole numbers in mhc_moe_sort, whose order cannot matter); the same
  *    inputs give bitwise identical outputs run to run.
  *  - A kernel that detects an internal fault (a bounded wait that timed
  *    out) sets a device-side error word and returns early;
