@@ -794,7 +794,8 @@ __global__ void __launch_bounds__(BwdTc<N>::THREADS, 1)
             // TMEM with du.W^T from the fp32 values before the usual reads below
             auto part_and_acc = [&](uint64_t *bar) -> bool {
                 if (*abort_v ||
-                    !tc::mbar_wait(bar, (i / P::STAGES) & 1, a.fault, tc::kFaultTimeoutFull) ||
+                    (bar &&
+                     !tc::mbar_wait(bar, (i / P::STAGES) & 1, a.fault, tc::kFaultTimeoutFull)) ||
                     !tc::mbar_wait(&d2full[b], (i >> 1) & 1, a.fault, tc::kFaultTimeoutAcc))
                     return false;
                 tc::tc_fence_after();
@@ -817,8 +818,12 @@ __global__ void __launch_bounds__(BwdTc<N>::THREADS, 1)
                 }
                 return true;
             };
-            // n = 4: dout and dy (the G part) and the accumulator before the mix
-            if (P::SPLIT && !part_and_acc(&gsfull[s])) {
+            // n = 4: dout and dy (the G part) and the accumulator before the mix.
+            // Without the layer terms the epilogue reads nothing of the G part
+            // and does not hold it back (gsempty counts the MMAs alone): tile
+            // i + 2's may land before a late warp looks for tile i's, and its
+            // wait would then be for tile i + 4's, which waits for that warp.
+            if (P::SPLIT && !part_and_acc(LAYER ? &gsfull[s] : nullptr)) {
                 ok = false;
                 if (P::STAGE_P) continue;
                 break;
