@@ -437,8 +437,8 @@ typedef enum { MHC_BF16 = 0, MHC_FP16 = 1, MHC_FP32 = 2 } mhc_dtype;
  *   y_i = a_i cos[pos][p] - a_j sin[pos][p],  y_j = a_j cos[pos][p] + a_i sin[pos][p];
  *   y = a for the elements past R.
  * gamma_q, gamma_k [D] fp32 (NULL: 1); cos, sin [P, R/2] fp32; pos [T] int32,
- * each in [0, P) (NULL: pos = t, T <= P); 1 <= D <= 512, 0 <= R <= D even
- * (R = 0: no rotation; cos, sin unused).  A token whose position is outside
+ * each in [0, P) (NULL: pos = t, T <= P); T, P < 2^31, 1 <= D <= 512,
+ * 0 <= R <= D even (R = 0: no rotation; cos, sin unused).  A token whose position is outside
  * the table gets zeros (device error 201).
  * strides: 8 element strides in HOST memory, (token, head) of q, k, q_out,
  * k_out in this order, or NULL: all contiguous [T, H, D].  The D elements of

@@ -10,8 +10,11 @@ has not been built (``python -m layers_proj_rms_gb300.build``).
 
 Tensor conventions (see include/mhc.h): x [T, n, C] bf16, W [n*C, O] fp32,
 alpha3 [3] fp32, b [O] fp32, H_pre/H_post [T, n] fp32, H_res [T, n, n] fp32,
-u_save [T, O] fp32, r_save [T] fp32, with O = n*n + 2*n.  Outputs are
-passed in preallocated; the library writes every element.
+u_save [T, O] fp32, r_save [T] fp32, with O = n*n + 2*n.  The operators at
+the edges of the sub-layers (mhc_qk_norm_rope_*, mhc_moe_*) take bf16, fp16 or
+fp32 activations, fp32 gammas, tables and router weights, int32 indices; q, k
+[T, H, D] may be views with any token and head strides.  Outputs are passed in
+preallocated; the library writes every element.
 """
 from __future__ import annotations
 

@@ -35,6 +35,8 @@ OP_QK_NORM_ROPE_BWD = 13
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
 
+_Tensor = torch.Tensor
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I = ctypes.c_int
@@ -129,7 +131,7 @@ def _ptr(t, dtype=None, shape=None, name="tensor"):
     if t is None:
         return None
     # the usual case in one test (a call of a small operator costs its marshalling)
-    if (type(t) is torch.Tensor and (dtype is None or t.dtype is dtype)
+    if (type(t) is _Tensor and (dtype is None or t.dtype is dtype)
             and (shape is None or t.shape == shape) and t.is_cuda and t.is_contiguous()):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
@@ -151,12 +153,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _device = getattr(torch._C, "_cuda_getDevice", None)
 
 
+_ready = False  # CUDA is initialised, and stays so
+
+
 def _stream(stream):
-    if stream is None:
-        if _raw_stream and _device and torch.cuda.is_initialized():
-            return _raw_stream(_device())
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    global _ready
+    if stream is not None:
+        return stream.cuda_stream
+    if not _ready:
+        if not (_raw_stream and _device and torch.cuda.is_initialized()):
+            return torch.cuda.current_stream().cuda_stream
+        _ready = True
+    return _raw_stream(_device())
 
 
 _BF, _F32 = torch.bfloat16, torch.float32
@@ -491,7 +499,7 @@ def _heads(t, dtype, shape, name):
     """Pointer and (token, head) strides of a [T, H, D] tensor or view."""
     if t is None and not shape[1]:
         return None, (0, 0)
-    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda:
+    if type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda:
         st = t.stride()
         if st[2] == 1:
             return t.data_ptr(), st[:2]

@@ -321,7 +321,7 @@ cudaError_t qk_ring_bwd(const QkArgs &a, float *part, int *blocks, cudaStream_t 
 
 // Blocks of a launch: as many as stay resident, `per_sm` on each SM.
 constexpr int qk_blocks(int per_sm) { return kSplitSms * per_sm; }
-constexpr int kQkBwdMaxBlocks = qk_blocks(4);  // rows of partials in the workspace
+constexpr int kQkBwdMaxBlocks = qk_blocks(2);  // rows of partials in the workspace
 QkGeom qk_geom(const QkArgs &a, int V, int K, int hpi, int max_blocks, int *blocks);
 
 }  // namespace mhc

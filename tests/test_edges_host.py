@@ -33,7 +33,7 @@ def L(M):
 # (keyword arguments, status): 1 null, 2 shape, 3 alignment, 6 argument
 @pytest.mark.parametrize("kw,status", [
     ({"dtype": 3}, 6), ({"dtype": -1}, 6), ({"T": -1}, 2), ({"Hq": -1}, 2), ({"D": 0}, 2),
-    ({"D": 513}, 2), ({"R": 65}, 2), ({"R": 33}, 2), ({"R": -2}, 2), ({"P": -1}, 2),
+    ({"D": 513}, 2), ({"R": 65}, 2), ({"R": 33}, 2), ({"R": -2}, 2), ({"P": -1}, 2), ({"T": 1 << 31}, 2), ({"P": 1 << 31}, 2),
     ({"eps": float("nan")}, 6), ({"eps": -1.0}, 6), ({"q": None}, 1), ({"ko": None}, 1),
     ({"cos": None}, 1), ({"sin": None}, 1), ({"q": A + 1}, 3), ({"dtype": 2, "k": A + 2}, 3),
     ({"gq": A + 4}, 3), ({"pos": A + 2}, 3), ({"pos": None, "T": 17}, 2),
