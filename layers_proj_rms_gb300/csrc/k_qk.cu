@@ -372,12 +372,20 @@ constexpr int kFwdHeads = 2, kFwdPerSm = 3;
 // a head: 19.8).
 constexpr int kNarrowHeads = 2, kNarrowPerSm = 3;
 
+// Whether one head per lane group holds all heads of q and of k (then two would
+// only work on heads that are not there).
+bool qk_few(const QkArgs &a, int V, int K)
+{
+    const int ng = 32 >> qk_lanes(a.D, V, K);
+    return a.m[0].H <= ng && a.m[1].H <= ng;
+}
+
 template <class T>
 cudaError_t fwd_of(const QkArgs &a, cudaStream_t s)
 {
     switch (qk_vec(a, int(sizeof(T)))) {
     case 8:
-        if (!qk_many(a)) return run_fwd<T, 8, 1, 1, 3>(a, s);
+        if (!qk_many(a) || qk_few(a, 8, 1)) return run_fwd<T, 8, 1, 1, 3>(a, s);
         if constexpr (sizeof(T) == 2) {
             constexpr int h = kFwdHeads, b = kFwdPerSm;
             const bool all = a.R == a.D;
@@ -389,9 +397,13 @@ cudaError_t fwd_of(const QkArgs &a, cudaStream_t s)
         }
         return run_fwd<T, 8, 1, kFwdHeads, kFwdPerSm>(a, s);
     case 2:
-        if (a.D <= 64) return run_fwd<T, 2, 2, kNarrowHeads, kNarrowPerSm>(a, s);
-        return a.D <= 96 ? run_fwd<T, 2, 3, kNarrowHeads, kNarrowPerSm>(a, s)
-                         : run_fwd<T, 2, 4, 1, 3>(a, s);
+        if (a.D <= 64)
+            return qk_few(a, 2, 2) ? run_fwd<T, 2, 2, 1, kNarrowPerSm>(a, s)
+                                   : run_fwd<T, 2, 2, kNarrowHeads, kNarrowPerSm>(a, s);
+        if (a.D <= 96)
+            return qk_few(a, 2, 3) ? run_fwd<T, 2, 3, 1, kNarrowPerSm>(a, s)
+                                   : run_fwd<T, 2, 3, kNarrowHeads, kNarrowPerSm>(a, s);
+        return run_fwd<T, 2, 4, 1, 3>(a, s);
     default:
         return a.D <= 128 ? run_fwd<T, 1, 4, 1, 3>(a, s) : run_fwd<T, 1, 8, 1, 2>(a, s);
     }
@@ -422,9 +434,7 @@ cudaError_t bwd_of(const QkArgs &a, float *ws, cudaStream_t s)
 QkGeom qk_geom(const QkArgs &a, int V, int K, int hpi, int max_blocks, int *blocks)
 {
     QkGeom g;
-    const int units = (a.D + 2 * V - 1) / (2 * V);
-    g.lg = 0;
-    while (g.lg < 5 && (K << g.lg) < units) ++g.lg;
+    g.lg = qk_lanes(a.D, V, K);
     const int per = (32 >> g.lg) * hpi;
     for (int i = 0; i < 2; ++i) g.nb[i] = (a.m[i].H + per - 1) / per;
     const int64_t nb = g.nb[0] + g.nb[1];

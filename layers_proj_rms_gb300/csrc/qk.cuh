@@ -322,6 +322,14 @@ cudaError_t qk_ring_bwd(const QkArgs &a, float *part, int *blocks, cudaStream_t 
 // Blocks of a launch: as many as stay resident, `per_sm` on each SM.
 constexpr int qk_blocks(int per_sm) { return kSplitSms * per_sm; }
 constexpr int kQkBwdMaxBlocks = qk_blocks(2);  // rows of partials in the workspace
+// log2 of the lanes of a head: K units of two chunks of V elements each.
+inline int qk_lanes(int D, int V, int K)
+{
+    const int units = (D + 2 * V - 1) / (2 * V);
+    int lg = 0;
+    while (lg < 5 && (K << lg) < units) ++lg;
+    return lg;
+}
 QkGeom qk_geom(const QkArgs &a, int V, int K, int hpi, int max_blocks, int *blocks);
 
 }  // namespace mhc
