@@ -1,8 +1,10 @@
-"""ctypes marshalling for libmhc (include/mhc.h)."""
+"""Marshalling for libmhc (include/mhc.h): ctypes, and csrc/marshal.c for the
+operators that are also called on single tokens."""
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -473,78 +475,36 @@ def mhc_proj_rms_partial_bwd(x_shard, W_shard, du, coef, dx_shard, dW_shard, ws,
 
 
 # ---------------------------------------------------------------------------
-# the entry of attention, mixture of experts
+# the entry of attention, mixture of experts (marshalled by csrc/marshal.c)
 # ---------------------------------------------------------------------------
 
-_I32 = torch.int32
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+def _load_marshal():
+    path = os.path.join(_HERE, "_build", "_marshal.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_marshal.so is missing ({path}); build it first with "
+                          "`python -m layers_proj_rms_gb300.build`")
+    name = __package__ + "._marshal" if __package__ else "_marshal"
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    m = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
+    loader.exec_module(m)
+    entries = ("mhc_qk_norm_rope_fwd", "mhc_qk_norm_rope_bwd", "mhc_moe_router_fwd",
+               "mhc_moe_router_bwd", "mhc_moe_sort", "mhc_moe_dispatch_fwd", "mhc_moe_dispatch_bwd",
+               "mhc_moe_combine_fwd", "mhc_moe_combine_bwd")
+    m.setup(torch.Tensor,
+            (torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8),
+            tuple(ctypes.cast(getattr(lib, n), _P).value for n in entries))
+    return m
 
 
-def _act(t, name):
-    """The library's code of an activation tensor's dtype."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected bfloat16, float16 or float32")
-    return code
+_marshal = _load_marshal()
 
 
-def _act_ptr(t, name):
-    code = _act(t, name)
-    return _ptr(t, name=name), code
-
-
-def _heads(t, dtype, shape, name):
-    """Pointer and (token, head) strides of a [T, H, D] tensor or view."""
-    if t is None and not shape[1]:
-        return None, (0, 0)
-    if type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.is_cuda:
-        st = t.stride()
-        if st[2] == 1:
-            return t.data_ptr(), st[:2]
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    st = t.stride()
-    if st[2] != 1 and shape[2] > 1:
-        raise ValueError(f"{name}: the elements of a head must be contiguous")
-    if not t.numel():
-        return None, (0, 0)
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.data_ptr(), st[:2]
-
-
-def _qk_shapes(q, k, cos):
-    """dtype code and dtype, shapes of q and k, R and P."""
-    one = k if q is None else q
-    if one is None:
-        raise ValueError("q and k are both None")
-    code = _act(one, "k" if q is None else "q")
-    dt, shape = one.dtype, one.shape
-    if len(shape) != 3:
-        raise ValueError(f"{'k' if q is None else 'q'} must be a [T, H, D] tensor")
-    T, H, D = shape
-    sq = (T, 0, D) if q is None else (T, H, D)
-    sk = (T, 0, D)
-    if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != 3:
-            raise ValueError("k must be a [T, H, D] tensor")
-        sk = (T, k.shape[1], D)
-    if cos is None:
-        return code, dt, sq, sk, 0, 0
-    P, half = cos.shape
-    return code, dt, sq, sk, 2 * half, P
-
-
-@functools.lru_cache(maxsize=256)
-def _strides(*values):
-    """The C array of a call's strides (made once for the same values)."""
-    return (ctypes.c_int64 * len(values))(*values)
+def _handle(stream):
+    """_stream(stream), before the arguments are looked at: without a GPU it is
+    they that are refused (no tensor can be on one)."""
+    if _ready or stream is not None or torch.cuda.is_available():
+        return _stream(stream)
+    return 0
 
 
 def mhc_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, cos, sin, pos, eps, q_out, k_out,
@@ -552,55 +512,22 @@ def mhc_qk_norm_rope_fwd(q, k, gamma_q, gamma_k, cos, sin, pos, eps, q_out, k_ou
     """q [T, Hq, D], k [T, Hk, D] and the outputs may be views with any token
     and head strides (slices of a packed qkv product, [H, T, D] layouts);
     q or k may be None; cos and sin None: no rotation."""
-    code, dt, sq, sk, R, P = _qk_shapes(q, k, cos)
-    T, Hq, D = sq
-    pq, a = _heads(q, dt, sq, "q")
-    pk, b = _heads(k, dt, sk, "k")
-    oq, c = _heads(q_out, dt, sq, "q_out")
-    ok, d = _heads(k_out, dt, sk, "k_out")
-    _ok(lib.mhc_qk_norm_rope_fwd(
-        pq, pk, code, _strides(*a, *b, *c, *d),
-        _ptr(gamma_q, _F32, (D,), "gamma_q"), _ptr(gamma_k, _F32, (D,), "gamma_k"),
-        _ptr(cos, _F32, (P, R // 2), "cos"), _ptr(sin, _F32, (P, R // 2), "sin"),
-        _ptr(pos, _I32, (T,), "pos"), T, Hq, sk[1], D, R, P, interleaved, eps, oq, ok,
-        _stream(stream)))
+    _ok(_marshal.qk_fwd(q, k, gamma_q, gamma_k, cos, sin, pos, eps, q_out, k_out, interleaved,
+                        _handle(stream)))
 
 
 def mhc_qk_norm_rope_bwd(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, pos, eps, dq, dk,
                          dgamma_q=None, dgamma_k=None, ws=None, interleaved=False, stream=None):
-    code, dt, sq, sk, R, P = _qk_shapes(q, k, cos)
-    T, Hq, D = sq
-    pu, a = _heads(dq_out, dt, sq, "dq_out")
-    pv, b = _heads(dk_out, dt, sk, "dk_out")
-    pq, c = _heads(q, dt, sq, "q")
-    pk, d = _heads(k, dt, sk, "k")
-    oq, e = _heads(dq, dt, sq, "dq")
-    ok, f = _heads(dk, dt, sk, "dk")
-    wp, wb = _ws(ws)
-    _ok(lib.mhc_qk_norm_rope_bwd(
-        pu, pv, pq, pk, code, _strides(*a, *b, *c, *d, *e, *f),
-        _ptr(gamma_q, _F32, (D,), "gamma_q"), _ptr(gamma_k, _F32, (D,), "gamma_k"),
-        _ptr(cos, _F32, (P, R // 2), "cos"), _ptr(sin, _F32, (P, R // 2), "sin"),
-        _ptr(pos, _I32, (T,), "pos"), T, Hq, sk[1], D, R, P, interleaved, eps, oq, ok,
-        _ptr(dgamma_q, _F32, (D,), "dgamma_q"), _ptr(dgamma_k, _F32, (D,), "dgamma_k"), wp, wb,
-        _stream(stream)))
+    _ok(_marshal.qk_bwd(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, pos, eps, dq, dk, dgamma_q,
+                        dgamma_k, ws, interleaved, _handle(stream)))
 
 
 def mhc_moe_router_fwd(logits, score, renorm, scale, ids, w, stream=None):
-    T, E = logits.shape
-    k = ids.shape[1]
-    _ok(lib.mhc_moe_router_fwd(
-        *_act_ptr(logits, "logits"), T, E, k, score, bool(renorm), scale,
-        _ptr(ids, _I32, (T, k), "ids"), _ptr(w, _F32, (T, k), "w"), _stream(stream)))
+    _ok(_marshal.router_fwd(logits, score, renorm, scale, ids, w, _handle(stream)))
 
 
 def mhc_moe_router_bwd(dw, logits, ids, score, renorm, scale, dlogits, stream=None):
-    T, E = logits.shape
-    k = ids.shape[1]
-    _ok(lib.mhc_moe_router_bwd(
-        _ptr(dw, _F32, (T, k), "dw"), *_act_ptr(logits, "logits"),
-        _ptr(ids, _I32, (T, k), "ids"), T, E, k, score, bool(renorm), scale,
-        _ptr(dlogits, logits.dtype, (T, E), "dlogits"), _stream(stream)))
+    _ok(_marshal.router_bwd(dw, logits, ids, score, renorm, scale, dlogits, _handle(stream)))
 
 
 def mhc_moe_rows(T: int, k: int, E: int, align: int) -> int:
@@ -609,49 +536,23 @@ def mhc_moe_rows(T: int, k: int, E: int, align: int) -> int:
 
 
 def mhc_moe_sort(ids, align, counts, offsets, row_of, slot_of, stream=None):
-    T, k = ids.shape
-    E, R = counts.shape[0], slot_of.shape[0]
-    _ok(lib.mhc_moe_sort(
-        _ptr(ids, _I32, name="ids"), T, k, E, align, R, _ptr(counts, _I32, (E,), "counts"),
-        _ptr(offsets, _I32, (E + 1,), "offsets"), _ptr(row_of, _I32, (T, k), "row_of"),
-        _ptr(slot_of, _I32, (R,), "slot_of"), _stream(stream)))
+    _ok(_marshal.sort(ids, align, counts, offsets, row_of, slot_of, _handle(stream)))
 
 
 def mhc_moe_dispatch_fwd(x, row_of, slot_of, xs, stream=None):
-    T, C = x.shape
-    k, R = row_of.shape[1], xs.shape[0]
-    _ok(lib.mhc_moe_dispatch_fwd(
-        *_act_ptr(x, "x"), _ptr(row_of, _I32, (T, k), "row_of"),
-        _ptr(slot_of, _I32, (R,), "slot_of"), T, k, R, C, _ptr(xs, x.dtype, (R, C), "xs"),
-        _stream(stream)))
+    _ok(_marshal.dispatch_fwd(x, row_of, slot_of, xs, _handle(stream)))
 
 
 def mhc_moe_dispatch_bwd(dxs, row_of, dx, stream=None):
-    R, C = dxs.shape
-    T, k = row_of.shape
-    _ok(lib.mhc_moe_dispatch_bwd(
-        *_act_ptr(dxs, "dxs"), _ptr(row_of, _I32, name="row_of"), T, k, R, C,
-        _ptr(dx, dxs.dtype, (T, C), "dx"), _stream(stream)))
+    _ok(_marshal.dispatch_bwd(dxs, row_of, dx, _handle(stream)))
 
 
 def mhc_moe_combine_fwd(ys, w, row_of, f, stream=None):
-    R, C = ys.shape
-    T, k = row_of.shape
-    _ok(lib.mhc_moe_combine_fwd(
-        *_act_ptr(ys, "ys"), _ptr(w, _F32, (T, k), "w"),
-        _ptr(row_of, _I32, name="row_of"), T, k, R, C, _ptr(f, ys.dtype, (T, C), "f"),
-        _stream(stream)))
+    _ok(_marshal.combine_fwd(ys, w, row_of, f, _handle(stream)))
 
 
 def mhc_moe_combine_bwd(df, ys, w, row_of, slot_of, dys, dw=None, stream=None):
-    code = _act(dys, "dys")
-    R, C = dys.shape
-    T, k = row_of.shape
-    _ok(lib.mhc_moe_combine_bwd(
-        _ptr(df, dys.dtype, (T, C), "df"), _ptr(ys, dys.dtype, (R, C), "ys"), code,
-        _ptr(w, _F32, (T, k), "w"), _ptr(row_of, _I32, name="row_of"),
-        _ptr(slot_of, _I32, (R,), "slot_of"), T, k, R, C, _ptr(dys, name="dys"),
-        _ptr(dw, _F32, (T, k), "dw"), _stream(stream)))
+    _ok(_marshal.combine_bwd(df, ys, w, row_of, slot_of, dys, dw, _handle(stream)))
 
 
 def mhc_set_batch_invariant(on: bool) -> None:

@@ -2,7 +2,8 @@
 
 Each translation unit under csrc/ is compiled in parallel to an object file,
 then linked (CUDA runtime linked statically) into
-layers_proj_rms_gb300/_build/libmhc.so.  Rebuilds only what changed.
+layers_proj_rms_gb300/_build/libmhc.so; gcc builds the binding's C part,
+_build/_marshal.so.  Rebuilds only what changed.
 """
 from __future__ import annotations
 
@@ -10,11 +11,13 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libmhc.so")
+MARSHAL = os.path.join(OUT, "_marshal.so")  # the binding's C part (csrc/marshal.c)
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -47,6 +50,20 @@ def _compile(src: str, obj: str, extra) -> None:
     os.replace(obj + ".tmp", obj)
 
 
+def _build_marshal(force: bool) -> None:
+    src = os.path.join(CSRC, "marshal.c")
+    newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "mhc.h")))
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = [shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", src, "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed for marshal.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     os.makedirs(OUT, exist_ok=True)
     hdr = _headers_mtime()
@@ -70,6 +87,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, LIB)
+    _build_marshal(force)
     if verbose:
         print(f"libmhc: {LIB}")
     return LIB

@@ -145,3 +145,38 @@ def test_binding_refuses(M):
                                None)
     with pytest.raises(TypeError, match="dtype"):
         M.mhc_moe_dispatch_fwd(x[0].int(), x[0].int(), x[0].int(), x[0].int())
+
+
+def test_binding_names_what_is_wrong(M):
+    """Types, shapes, dimensions, missing tensors: each refused by name before a
+    device is looked at (the tensors here are on the CPU)."""
+    i32, bf = torch.int32, torch.bfloat16
+    meta = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device="meta")  # noqa: E731
+    ids, w, cnt, off = meta(4, 2, dt=i32), meta(4, 2), meta(5, dt=i32), meta(6, dt=i32)
+    row, slot = meta(4, 2, dt=i32), meta(8, dt=i32)
+    with pytest.raises(TypeError, match="ids must be a torch.Tensor"):
+        M.mhc_moe_sort([[1]], 1, cnt, off, row, slot)
+    with pytest.raises(TypeError, match="counts must be a torch.Tensor"):
+        M.mhc_moe_sort(ids, 1, None, off, row, slot)
+    with pytest.raises(ValueError, match="CUDA"):
+        M.mhc_moe_sort(ids, 1, cnt, off, row, slot)
+    with pytest.raises(TypeError, match="ids: dtype torch.int64, expected torch.int32"):
+        M.mhc_moe_sort(ids.long(), 1, cnt, off, row, slot)
+    with pytest.raises(ValueError, match="2 dimensions"):
+        M.mhc_moe_sort(cnt, 1, cnt, off, row, slot)
+    e = torch.empty(0, dtype=i32)
+    with pytest.raises(ValueError, match=r"offsets: shape .*expected \(1,\)"):
+        M.mhc_moe_sort(e.view(0, 2), 1, e, e, e.view(0, 2), e)
+    logits = meta(4, 8)
+    with pytest.raises(TypeError, match="logits: dtype torch.int32"):
+        M.mhc_moe_router_fwd(logits.int(), 0, True, 1.0, ids, w)
+    q = torch.empty(0, 2, 64, dtype=bf)
+    with pytest.raises(ValueError, match="both None"):
+        M.mhc_qk_norm_rope_fwd(None, None, None, None, None, None, None, EPS, None, None)
+    with pytest.raises(TypeError, match="q_out must be a torch.Tensor"):
+        M.mhc_qk_norm_rope_fwd(q, None, None, None, None, None, None, EPS, None, None)
+    with pytest.raises(TypeError, match="q_out: dtype torch.float32, expected torch.bfloat16"):
+        M.mhc_qk_norm_rope_fwd(q, None, None, None, None, None, None, EPS, q.float(), None)
+    with pytest.raises(ValueError, match=r"q_out: shape .*expected \(0, 2, 64\)"):
+        M.mhc_qk_norm_rope_fwd(q, None, None, None, None, None, None, EPS, q[:, :1], None)
+    M.mhc_qk_norm_rope_fwd(q, None, None, None, None, None, None, EPS, q, None)  # no tokens
