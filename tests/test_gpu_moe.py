@@ -101,6 +101,24 @@ def test_router_bf16_ties_are_common_and_exact(M):
     assert np.array_equal(ids.cpu().numpy(), O.top(O.np64(l), 8))
 
 
+@pytest.mark.parametrize("E,k", [(64, 4), (200, 8), (256, 8), (1024, 32)])
+def test_router_logits_that_differ_in_their_last_bits(M, E, k):
+    """fp32 logits a few steps apart (all, or some at the border of the choice),
+    and every kind of 16-bit pattern."""
+    g = rng(E)
+    near = torch.stack([torch.randperm(E, generator=g) for _ in range(40)]).int()
+    base = torch.tensor([1.0, -1.0, 3e-39, 2.5e38]).view(torch.int32).repeat(10)[:, None]
+    l = (base + near).view(torch.float32)
+    l[10:20] = torch.where(near[10:20] % 3 == 0, l[10:20], torch.randn(10, E, generator=g))
+    ids, w = route(M, l.cuda(), k, "softmax", True)
+    assert np.array_equal(ids.cpu().numpy(), O.top(l.double().numpy(), k))
+    for dt in (torch.bfloat16, torch.float16):
+        bits = torch.randint(-32768, 32768, (200, E), generator=g).to(torch.int16).view(dt)
+        bits = torch.where(bits.isfinite(), bits, torch.zeros((), dtype=dt))
+        ids, _ = route(M, bits.cuda(), k, "sigmoid", False)
+        assert np.array_equal(ids.cpu().numpy(), O.top(bits.double().numpy(), k))
+
+
 def plan(M, ids, E, align, R=None):
     T, k = ids.shape
     R = M.mhc_moe_rows(T, k, E, align) if R is None else R
