@@ -421,7 +421,8 @@ MHC_API mhc_status mhc_h_post_bda_compute_h_fwd(
 /* kernels check each before they use it, leave it out and set the      */
 /* device error word (201 a position outside the table, 202 an expert   */
 /* outside [-1, E) in mhc_moe_sort, 203 a row outside [-1, R), 204 an   */
-/* expert outside [-1, E) in mhc_moe_router_bwd).                       */
+/* expert outside [-1, E), or not of the forward's choice, in           */
+/* mhc_moe_router_bwd).                                                 */
 /* A token's results do not depend on T or on its place in the batch;   */
 /* the batch-invariant and the bit-reproducible mode change nothing here.*/
 /* ------------------------------------------------------------------ */
@@ -489,7 +490,11 @@ MHC_API mhc_status mhc_moe_router_fwd(const void *logits, mhc_dtype dtype, int64
                                       int32_t *ids, float *w, mhc_stream_t stream);
 
 /* dlogits [T, E] (type of the logits) from dw [T, k] fp32, the logits and
- * ids of the forward; an id of -1 (a dropped slot) carries no gradient. */
+ * ids of the forward.  A slot dropped after the choice may have its id set to
+ * -1: its dw counts as 0, and with renorm its score stays in the weights' sum,
+ * which the forward formed over the whole choice (in any order of the slots).
+ * With renorm, an id of a row with such a slot that is not among the k
+ * largest logits is left out and sets device error 204. */
 MHC_API mhc_status mhc_moe_router_bwd(const float *dw, const void *logits, mhc_dtype dtype,
                                       const int32_t *ids, int64_t T, int E, int k,
                                       mhc_score score, int renorm, float scale, void *dlogits,

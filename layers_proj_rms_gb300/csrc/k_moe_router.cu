@@ -12,7 +12,10 @@
 //     softmax, renorm:  dl_j = v_j (a_j - sum_i a_i v_i), v = w / scale
 //     sigmoid:          dl_j = a_j s_j (1 - s_j)
 //     sigmoid, renorm:  dl_j = v_j (1 - s_j) (a_j - sum_i a_i v_i)
-//   dlogits of the experts not chosen are 0 but for the plain softmax.
+//   dlogits of the experts not chosen are 0 but for the plain softmax.  A slot
+//   dropped after the choice (id -1) has a_j = 0; renormalised, its score stays
+//   in the weights' sum, as in the forward, so a row with such a slot is chosen
+//   again (the choice is exact) and its experts' dl_j have their share of it.
 //
 // One warp per token; lane l holds logits l, l + 32, ...  The choice compares
 // logits as stored (monotone integer keys), never computed scores, so it is
@@ -24,7 +27,9 @@
 
 namespace mhc {
 
-constexpr int kFaultChoice = 204;  // backward: an id outside [-1, E)
+// backward: an id outside [-1, E), or one that the forward did not choose in a
+// row whose choice has to be found again
+constexpr int kFaultChoice = 204;
 
 namespace {
 
@@ -140,7 +145,7 @@ __device__ __forceinline__ void sort_desc(unsigned (&p)[NV])
 }
 
 // The choice packs a logit's key and its index into one word: the key's upper
-// upper 22 bits over 1023 - index, so that one integer maximum finds the
+// 22 bits over 1023 - index, so that one integer maximum finds the
 // largest logit and, among equal ones, the lowest index.  22 bits hold the
 // whole of a bf16 or fp16 value (16 and 19 bits of its fp32 form).  Of a
 // 32-bit logit they do not: the order is then certain unless two neighbours of
@@ -272,8 +277,22 @@ __global__ void __launch_bounds__(kRouterWarps * 32)
         report_fault(fault, kFaultChoice);
         id = -1;
     }
+    float a = id >= 0 ? scale * __ldg(dw + t * k + lane) : 0.f;
+    if (renorm && __any_sync(kFull, lane < k && id < 0)) {
+        // lane j takes choice j, and the gradient of the slot that kept it
+        const int found = choose_exact<T, NV, false>(row, E, k), chosen = lane < k ? found : -1;
+        float kept = 0.f;
+        for (int j = 0; j < k; ++j) {
+            const int e = __shfl_sync(kFull, id, j);
+            const float v = __shfl_sync(kFull, a, j);
+            if (e < 0) continue;
+            if (e == chosen) kept += v;
+            if (!__any_sync(kFull, e == chosen)) report_fault(fault, kFaultChoice);
+        }
+        id = chosen;
+        a = kept;
+    }
     const bool on = id >= 0;
-    const float a = on ? scale * __ldg(dw + t * k + lane) : 0.f;
     const float lj = on ? widen1(row[id]) : -INFINITY;
     float d;         // this lane's slot's gradient
     float out[NV];   // dlogits of experts lane, lane + 32, ...

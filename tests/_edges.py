@@ -113,12 +113,22 @@ def softmax(v, on):
     return p / np.where(s == 0, 1, s)
 
 
+def choice(l, ids):
+    """The forward's ids where some may since have been dropped (-1)."""
+    ids = np.where(ids < 0, top(l, ids.shape[1]), ids)
+    assert all(len(set(row)) == len(row) for row in ids.tolist())
+    return ids
+
+
 def router_scores(l, ids, score, renorm):
-    """Weights (scale 1) of the chosen slots; ids -1: none."""
+    """Weights (scale 1) of the chosen slots; ids -1: dropped after the choice,
+    0, but part of the sum that the weights are renormalised by."""
     on = ids >= 0
     lj = np.where(on, np.take_along_axis(l, np.maximum(ids, 0), 1), -np.inf)
     if renorm:
-        return softmax(lj if score == "softmax" else -np.logaddexp(0, -lj), on)
+        lj = np.take_along_axis(l, choice(l, ids), 1)
+        v = softmax(lj if score == "softmax" else -np.logaddexp(0, -lj), np.ones_like(on))
+        return np.where(on, v, 0)
     if score == "softmax":
         p = softmax(l, np.ones_like(l, bool))
         return np.where(on, np.take_along_axis(p, np.maximum(ids, 0), 1), 0)
@@ -128,8 +138,11 @@ def router_scores(l, ids, score, renorm):
 def router_bwd(dw, l, ids, score, renorm, scale):
     """dlogits and its magnitude."""
     on, at = ids >= 0, np.maximum(ids, 0)
-    v = router_scores(l, ids, score, renorm)
     a = np.where(on, scale * dw, 0)
+    if renorm:  # a dropped slot's expert has its share of the weights' sum
+        ids = at = choice(l, ids)
+        on = np.ones_like(on)
+    v = router_scores(l, ids, score, renorm)
     slope = logistic(-np.take_along_axis(l, at, 1)) if score == "sigmoid" else 1.0
     d, dm = np.zeros_like(l), np.zeros_like(l)
     if renorm or score == "softmax":
