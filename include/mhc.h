@@ -423,8 +423,9 @@ MHC_API mhc_status mhc_h_post_bda_compute_h_fwd(
 /* outside [-1, E) in mhc_moe_sort, 203 a row outside [-1, R), 204 an   */
 /* expert outside [-1, E), or not of the forward's choice, in           */
 /* mhc_moe_router_bwd).                                                 */
-/* A token's results do not depend on T or on its place in the batch;   */
-/* the batch-invariant and the bit-reproducible mode change nothing here.*/
+/* A token's results do not depend on T or on its place in the batch    */
+/* (for q/k: of tensors with the same strides, see there); the batch-   */
+/* invariant and the bit-reproducible mode change nothing here.         */
 /* ------------------------------------------------------------------ */
 
 typedef enum { MHC_BF16 = 0, MHC_FP16 = 1, MHC_FP32 = 2 } mhc_dtype;
@@ -445,8 +446,13 @@ typedef enum { MHC_BF16 = 0, MHC_FP16 = 1, MHC_FP32 = 2 } mhc_dtype;
  * k_out in this order, or NULL: all contiguous [T, H, D].  The D elements of
  * a head are contiguous.  q, k, q_out, k_out and pos need only the alignment
  * of their elements; 16-byte pointers and strides, D a multiple of 8 and R of
- * 16 take the fastest path.  q_out may be q and k_out k (same strides);
- * outputs must not overlap inputs otherwise.  Hq or Hk may be 0. */
+ * 16 take the fastest path.  The order of a head's sums goes by D, R and the
+ * alignment that the call's pointers and strides share (16 bytes, 4 for 16-bit
+ * types and 8 for fp32, or less), so layouts that differ in it may differ in
+ * last bits.  The token strides count for T = 1 too, so that a slice of
+ * some tokens has the bits that they have in the whole.  q_out may be q and
+ * k_out k (same strides); outputs must not overlap inputs otherwise.  Hq or Hk
+ * may be 0. */
 MHC_API mhc_status mhc_qk_norm_rope_fwd(const void *q, const void *k, mhc_dtype dtype,
                                         const int64_t *strides, const float *gamma_q,
                                         const float *gamma_k, const float *cos, const float *sin,

@@ -851,10 +851,12 @@ mhc_status mhc_proj_rms_partial_bwd(const mhc_bf16 *x_shard, const float *W_shar
 namespace {
 
 // Fills one of q, k; strides: (token, head) pairs of the tensors in `order`.
-// A tensor of which only one token or head exists has no stride to check.
-void qk_tensor(Check &ck, mhc::QkTensor &m, const char *name, int64_t T, int H, int D, int es,
-               const void *x, const int64_t *xs, const void *up, const int64_t *us, void *out,
-               const int64_t *os, const float *gamma, float *dgamma)
+// A tensor of which only one token or head exists has no stride to check, but
+// a token stride has its say in `bits` all the same: the order of a head's
+// sums goes by it, and must not change with the number of tokens.
+void qk_tensor(Check &ck, mhc::QkTensor &m, uint64_t &bits, const char *name, int64_t T, int H,
+               int D, int es, const void *x, const int64_t *xs, const void *up, const int64_t *us,
+               void *out, const int64_t *os, const float *gamma, float *dgamma)
 {
     const int64_t plain[2] = {int64_t(H) * D, D};
     xs = xs ? xs : plain;
@@ -882,6 +884,10 @@ void qk_tensor(Check &ck, mhc::QkTensor &m, const char *name, int64_t T, int H, 
     const bool same_up = (one_t || us[0] == os[0]) && (one_h || us[1] == os[1]);
     if ((out == x && !same) || (out == up && !same_up))
         bad(MHC_ERR_BAD_SHAPE, "a call in place needs the same strides");
+    for (const void *p : {x, up, static_cast<const void *>(out)})
+        bits |= reinterpret_cast<uintptr_t>(p);
+    for (const int64_t *st : {xs, up ? us : xs, os})
+        bits |= uint64_t(st[0] * es) | (one_h ? 0 : uint64_t(st[1] * es));
     if (one_t) m.x_t = m.up_t = m.out_t = 0;  // never used
     if (one_h) m.x_h = m.up_h = m.out_h = 0;
 }
@@ -930,9 +936,9 @@ mhc_status mhc_qk_norm_rope_fwd(const void *q, const void *k, mhc_dtype dtype,
     if (ck.st || T == 0 || Hq + Hk == 0) return ck.st;
     const int es = dtype == MHC_FP32 ? 4 : 2;
     const int64_t *st = strides;
-    qk_tensor(ck, a.m[0], "q", T, Hq, D, es, q, st, nullptr, nullptr, q_out, st ? st + 4 : st,
-              gamma_q, nullptr);
-    qk_tensor(ck, a.m[1], "k", T, Hk, D, es, k, st ? st + 2 : st, nullptr, nullptr, k_out,
+    qk_tensor(ck, a.m[0], a.bits, "q", T, Hq, D, es, q, st, nullptr, nullptr, q_out,
+              st ? st + 4 : st, gamma_q, nullptr);
+    qk_tensor(ck, a.m[1], a.bits, "k", T, Hk, D, es, k, st ? st + 2 : st, nullptr, nullptr, k_out,
               st ? st + 6 : st, gamma_k, nullptr);
     if (ck.device().st) return ck.st;
     a.fault = fault_ptr();
@@ -965,8 +971,10 @@ mhc_status mhc_qk_norm_rope_bwd(const void *dq_out, const void *dk_out, const vo
     auto at = [&](int i) { return st ? st + i : st; };
     if ((Hq && !dq_out) || (Hk && !dk_out))
         return fail(MHC_ERR_NULL_PTR, "%s: an upstream gradient is NULL", ck.fn);
-    qk_tensor(ck, a.m[0], "q", T, Hq, D, es, q, at(4), dq_out, at(0), dq, at(8), gamma_q, dgamma_q);
-    qk_tensor(ck, a.m[1], "k", T, Hk, D, es, k, at(6), dk_out, at(2), dk, at(10), gamma_k, dgamma_k);
+    qk_tensor(ck, a.m[0], a.bits, "q", T, Hq, D, es, q, at(4), dq_out, at(0), dq, at(8), gamma_q,
+              dgamma_q);
+    qk_tensor(ck, a.m[1], a.bits, "k", T, Hk, D, es, k, at(6), dk_out, at(2), dk, at(10), gamma_k,
+              dgamma_k);
     if (dgamma_q || dgamma_k) ck.ws(ws, ws_bytes, mhc::qk_bwd_ws_bytes(T, Hq + Hk, D));
     if (ck.device().st) return ck.st;
     a.fault = fault_ptr();

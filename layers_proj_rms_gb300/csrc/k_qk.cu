@@ -18,9 +18,9 @@
 //
 // V = 8 (16-byte vectors for 16-bit types) needs R a multiple of 16, D of 8,
 // and strides and pointers on 16 bytes; V = 2 needs R a multiple of 4 and D
-// of 2; V = 1 takes anything (V = 4 was no faster than V = 2).  A lane of a head has K units (V = 8: one).  The
-// order of a head's sums is fixed by V, D and R: it depends neither on the
-// grid nor on T.
+// of 2; V = 1 takes anything (V = 4 was no faster than V = 2).  A lane of a head
+// has K units (V = 8: one).  The order of a head's sums is fixed by V, D and R:
+// it depends neither on the grid nor on T.
 //
 // What bounds it: HBM on long inputs, once the instructions are few enough for
 // 24 warps an SM to keep it busy: packed fp32 pairs, gamma folded into cos and
@@ -297,23 +297,13 @@ __global__ void __launch_bounds__(1024)
 // host side
 // ---------------------------------------------------------------------------
 
-bool on(const void *p, int64_t st, int64_t sh, int es, int bytes)
-{
-    return (reinterpret_cast<uintptr_t>(p) % bytes) == 0 && st * es % bytes == 0 &&
-           sh * es % bytes == 0;
-}
-
-// Elements of a chunk: the widest form whose rules the call meets.
+// Elements of a chunk: the widest form whose rules the call meets.  Nothing
+// here goes by T (the token strides count as given, for one token too).
 int qk_vec(const QkArgs &a, int es)
 {
     for (int v : {8, 2}) {
-        bool ok = a.D % v == 0 && (a.R / 2) % v == 0;
         const int bytes = v * es < 16 ? v * es : 16;
-        for (const QkTensor &m : a.m)
-            if (m.H > 0)
-                ok = ok && on(m.x, m.x_t, m.x_h, es, bytes) && on(m.out, m.out_t, m.out_h, es, bytes) &&
-                     (!m.up || on(m.up, m.up_t, m.up_h, es, bytes));
-        if (ok) return v;
+        if (a.D % v == 0 && (a.R / 2) % v == 0 && a.bits % bytes == 0) return v;
     }
     return 1;
 }

@@ -25,6 +25,7 @@ struct QkArgs {
     int64_t T, P;
     int D, R;
     int interleaved;
+    uint64_t bits;  // the pointers and the strides in bytes, as given, or-ed (their alignment)
     float eps;
     int *fault;
 };
