@@ -479,9 +479,10 @@ def mhc_proj_rms_partial_bwd(x_shard, W_shard, du, coef, dx_shard, dW_shard, ws,
 # ---------------------------------------------------------------------------
 
 def _load_marshal():
-    path = os.path.join(_HERE, "_build", "_marshal.so")
+    # the name has this Python's ABI: one built for another is not looked at
+    path = os.path.join(_HERE, "_build", "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
     if not os.path.exists(path):
-        raise ImportError(f"_marshal.so is missing ({path}); build it first with "
+        raise ImportError(f"the binding's C part is missing ({path}); build it first with "
                           "`python -m layers_proj_rms_gb300.build`")
     name = __package__ + "._marshal" if __package__ else "_marshal"
     loader = importlib.machinery.ExtensionFileLoader(name, path)
@@ -496,7 +497,17 @@ def _load_marshal():
     return m
 
 
-_marshal = _load_marshal()
+class _Unloaded:
+    """Stands for the C part until the first call that needs it: the entry
+    points above do without it."""
+
+    def __getattr__(self, name):
+        global _marshal
+        _marshal = _load_marshal()
+        return getattr(_marshal, name)
+
+
+_marshal = _Unloaded()
 
 
 def _handle(stream):

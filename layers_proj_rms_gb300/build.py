@@ -2,22 +2,26 @@
 
 Each translation unit under csrc/ is compiled in parallel to an object file,
 then linked (CUDA runtime linked statically) into
-layers_proj_rms_gb300/_build/libmhc.so; gcc builds the binding's C part,
-_build/_marshal.so.  Rebuilds only what changed.
+layers_proj_rms_gb300/_build/libmhc.so; gcc builds the binding's C part, which
+belongs to one Python ABI and says so in its name (_build/_marshal.cpython-...).
+Rebuilds only what changed.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.machinery
 import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libmhc.so")
-MARSHAL = os.path.join(OUT, "_marshal.so")  # the binding's C part (csrc/marshal.c)
+# the binding's C part (csrc/marshal.c)
+MARSHAL = os.path.join(OUT, "_marshal" + importlib.machinery.EXTENSION_SUFFIXES[0])
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -55,9 +59,14 @@ def _build_marshal(force: bool) -> None:
     newest = max(os.path.getmtime(src), os.path.getmtime(os.path.join(INCLUDE, "mhc.h")))
     if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
         return
+    headers = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(headers, "Python.h")):
+        warnings.warn(f"no Python.h in {headers}: mhc_qk_norm_rope_* and mhc_moe_* cannot be "
+                      "called from Python (their binding, csrc/marshal.c, is not built)")
+        return
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-I{sysconfig.get_paths()['include']}", f"-I{INCLUDE}", src, "-o", tmp]
+           f"-I{headers}", f"-I{INCLUDE}", src, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"gcc failed for marshal.c:\n{r.stdout}\n{r.stderr}")
