@@ -204,7 +204,9 @@ def backward(s, p, caches, dout):
 
 # ---- the same block in plain torch, fp32, with autograd ----------------------------
 
-def reference(s, p, x, ids):
+def reference(s, p, x, ids, through=lambda path, v: v):
+    """through(path, v) stands for v on one of the ways from x to the output (an
+    identity, but for its gradient if a caller wants to cut one)."""
     def controller(w, x):
         T, n, C = x.shape
         flat = x.flatten(1)
@@ -227,18 +229,20 @@ def reference(s, p, x, ids):
 
     for name in ("attn", "moe"):
         w = p[name]
-        pre, post, res = controller(w, x)
-        y = norm(torch.einsum("tn,tnc->tc", pre, x), w["gamma"])
+        at = lambda path, v: through(f"{name}.{path}", v)  # noqa: E731, B023
+        pre, post, res = (at(n, h) for n, h in zip(("H_pre", "H_post", "H_res"), controller(w, x)))
+        y = norm(torch.einsum("tn,tnc->tc", pre, at("aggregate", x)), w["gamma"])
         if name == "attn":
             q, k, v = (y @ w["Wqkv"]).view(s["T"], -1, s["D"]).split((s["Hq"], s["Hk"], s["Hk"]), 1)
+            q, k, v = at("q", q), at("k", k), at("v", v)
             f = attend(rope(norm(q, w["gamma_q"])), rope(norm(k, w["gamma_k"])), v).flatten(1) @ w["Wo"]
         else:
-            wt = (y @ w["Wr"]).gather(1, ids.long()).softmax(-1)
-            h = torch.einsum("tc,ecf->tef", y, w["W1"]).relu()
+            wt = (at("router", y) @ w["Wr"]).gather(1, ids.long()).softmax(-1)
+            h = torch.einsum("tc,ecf->tef", at("experts", y), w["W1"]).relu()
             each = torch.einsum("tef,efc->tec", h, w["W2"])
             f = torch.einsum("tk,tkc->tc", wt, each.gather(
                 1, ids.long()[..., None].expand(-1, -1, s["C"])))
-        x = torch.einsum("tji,tjc->tic", res, x) + post[..., None] * (f + w["bias"])[:, None]
+        x = torch.einsum("tji,tjc->tic", res, at("residual", x)) + post[..., None] * (f + w["bias"])[:, None]
     return x
 
 
