@@ -18,7 +18,8 @@
 // a slot's row is its segment's base + its rank, stable by construction.
 // Segments of up to 256 slots stay in registers; longer ones are walked twice.
 //
-// What bounds it: latency (a training step's 131072 slots are 0.5 MB).
+// What bounds it: latency (a training step's 131072 slots are 0.5 MB); far beyond
+// that, that each cluster counts all the slots of the others (1 M slots: 33 us).
 #include <cooperative_groups.h>
 
 #include "launch.h"
