@@ -431,7 +431,7 @@ def _own(s):
         M.mhc_fp8_wgrad(s["at"], s["sat"], s["bt"], s["sbt"], s["offsets"], s["out"])
         return {"out": s["out"]}
     if "ws" not in s:
-        s["ws"] = M.workspace(M.OP_MOE_FEW_FWD, c["T"], c["k"], c["F"])
+        s["ws"] = M.workspace(M.OP_MOE_FEW_FWD, c["T"], c["k"], c["C"] + c["F"])
     M.mhc_moe_few_fwd(s["x"], s["ids"], s["w"], s["w1"], s["w2"], s["f"], s["ws"], s["s1"],
                       s["s2"])
     return {"f": s["f"]}
