@@ -142,7 +142,8 @@ typedef enum {
     MHC_OP_COMPUTE_H_BWD = 10,
     MHC_OP_PROJ_RMS_PARTIAL_BWD = 11,  /* C = the shard's channels Cs */
     MHC_OP_H_POST_BDA_COMPUTE_H_FWD = 12,
-    MHC_OP_QK_NORM_ROPE_BWD = 13 /* (T, Hq + Hk, D); only when a dgamma is wanted */
+    MHC_OP_QK_NORM_ROPE_BWD = 13, /* (T, Hq + Hk, D); only when a dgamma is wanted */
+    MHC_OP_MOE_FEW_FWD = 14       /* (T, k, C + F) */
 } mhc_op;
 
 /* Workspace bytes an op needs for (T, n, C); 0 for a bad op or shape.
@@ -549,6 +550,94 @@ MHC_API mhc_status mhc_moe_combine_bwd(const void *df, const void *ys, mhc_dtype
                                        const float *w, const int32_t *row_of,
                                        const int32_t *slot_of, int64_t T, int k, int64_t R,
                                        int64_t C, void *dys, float *dw, mhc_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* The experts' products in 8-bit floating point, between the dispatch  */
+/* and the combine above: quantisation, the gated activation, the       */
+/* products and their gradients, and the whole layer for a few tokens.  */
+/* The web pages have no counterpart of these entry points.             */
+/*                                                                      */
+/* A quantised matrix holds 8-bit values along the dimension that a     */
+/* product reduces (its last, K), and a scale for each block of 128 of  */
+/* K (the last block may be shorter), for each row (s [blocks of K,     */
+/* rows]) or for each 128 rows (s [blocks of K, blocks of rows]): it    */
+/* stands for q * s.  Sums are fp32: a block's products by the tensor   */
+/* cores, exact but for their sum's rounding, then scaled and added in  */
+/* fp32; each result is rounded to its type once.                       */
+/* Segments: offsets [G + 1] int32 as mhc_moe_sort writes them, or NULL */
+/* (G = 1): all R rows.  Offsets that go back or leave [0, R] are taken */
+/* as the nearest that do not, and set device error 205.                */
+/* Outputs must not overlap inputs or each other.                       */
+/* ------------------------------------------------------------------ */
+
+typedef enum { MHC_E4M3 = 0, MHC_E5M2 = 1 } mhc_fp8;
+
+/* For x [G, R, C] of `dtype`: in each block amax = max(largest |x|, 2^-100),
+ * scale = amax / top, q = round(x * (top / amax)) to nearest even, top 448
+ * (e4m3) or 57344 (e5m2), in fp32.  A block with an infinity or a NaN has the
+ * scale NaN.  Either pair of outputs may be NULL:
+ *   q [G, R, C], s [G, blocks of C, R]:   blocks of 128 along C;
+ *   qt [G, C, R], st [G, blocks of R, C]: blocks of 128 along R, transposed;
+ * tiles: one scale for 128 x 128, q and qt the same values,
+ *   s [G, blocks of C, blocks of R], st [G, blocks of R, blocks of C].
+ * C a multiple of 16, with qt R too; G <= 65535. */
+MHC_API mhc_status mhc_fp8_quant(const void *x, mhc_dtype dtype, int64_t G, int64_t R, int64_t C,
+                                 mhc_fp8 format, int tiles, uint8_t *q, float *s, uint8_t *qt,
+                                 float *st, mhc_stream_t stream);
+
+/* a = silu(gate) up for h [R, 2F] = [gate | up], in fp32: a [R, F] rounded to
+ * `dtype` (NULL to skip) and quantised from the fp32 values as above, q [R, F]
+ * with s, qt [F, R] with st (each pair NULL to skip).  F a multiple of 16. */
+MHC_API mhc_status mhc_fp8_swiglu_fwd(const void *h, mhc_dtype dtype, int64_t R, int64_t F,
+                                      mhc_fp8 format, void *a, uint8_t *q, float *s, uint8_t *qt,
+                                      float *st, mhc_stream_t stream);
+
+/* dh [R, 2F] from da [R, F] and h: with p = sigmoid(gate),
+ *   dgate = da up p (1 + gate (1 - p)),  dup = da gate p;
+ * outputs as above, over the 2F columns [dgate | dup] (a block of 128 may
+ * hold both where F is no multiple of 128). */
+MHC_API mhc_status mhc_fp8_swiglu_bwd(const void *da, const void *h, mhc_dtype dtype, int64_t R,
+                                      int64_t F, mhc_fp8 format, void *dh, uint8_t *q, float *s,
+                                      uint8_t *qt, float *st, mhc_stream_t stream);
+
+/* out [R, N]: out[r][n] = sum_k a[r][k] b[e][n][k] for the rows r of segment
+ * e; rows of no segment are zeroed and not read.  a [R, K] with sa [blocks of
+ * K, R]; b [G, N, K] with sb [G, blocks of K, blocks of N].  The gradient of
+ * the rows is the same product with the transposed weights (qt, st of tiles).
+ * N a multiple of 8, K of 16, G <= MHC_MOE_MAX_EXPERTS. */
+MHC_API mhc_status mhc_fp8_gemm(const uint8_t *a, mhc_fp8 format_a, const float *sa,
+                                const uint8_t *b, mhc_fp8 format_b, const float *sb,
+                                const int32_t *offsets, int64_t G, int64_t R, int64_t N, int64_t K,
+                                mhc_dtype out_dtype, void *out, mhc_stream_t stream);
+
+/* out [G, M, N]: out[e][m][n] = sum over the rows r of segment e of
+ * at[m][r] bt[n][r], zero for an empty segment.  at [M, R] with sat [blocks
+ * of R, M], bt [N, R] with sbt [blocks of R, N] (qt, st of the rows' two
+ * matrices).  Segments start at multiples of 128 (sort with align 128; others
+ * are rounded down and set device error 206).  N a multiple of 8, R of 16. */
+MHC_API mhc_status mhc_fp8_wgrad(const uint8_t *at, mhc_fp8 format_a, const float *sat,
+                                 const uint8_t *bt, mhc_fp8 format_b, const float *sbt,
+                                 const int32_t *offsets, int64_t G, int64_t R, int64_t M,
+                                 int64_t N, mhc_dtype out_dtype, void *out, mhc_stream_t stream);
+
+#define MHC_MOE_FEW_TOKENS 128
+#define MHC_MOE_FEW_MAX_C 16384
+
+/* The experts' layer for a few tokens, without a sort:
+ *   f[t] = sum_j w[t][j] W2[e] (silu(Wg[e] x[t]) Wu[e] x[t]),  e = ids[t][j],
+ * j ascending; x, f [T, C] of `dtype` (bf16 or fp16), ids [T, k] int32 in
+ * [-1, E) (-1: a dropped slot, which adds nothing; any other value outside is
+ * dropped too and sets device error 202), w [T, k] fp32.  w1 [E, 2F, C] = [Wg;
+ * Wu], w2 [E, C, F]: of `dtype` (s1, s2 NULL), or e4m3 with scales by tiles,
+ * s1 [E, blocks of C, blocks of 2F], s2 [E, blocks of F, blocks of C]; then x
+ * and the activation are quantised to e4m3 by blocks of 128 as mhc_fp8_quant
+ * does, the latter from its fp32 values.  Each slot's sums are fp32 throughout.
+ * T <= 128, k <= 32, C and F multiples of 16 and <= 16384.
+ * ws: mhc_workspace_bytes(MHC_OP_MOE_FEW_FWD, T, k, C + F). */
+MHC_API mhc_status mhc_moe_few_fwd(const void *x, mhc_dtype dtype, const int32_t *ids,
+                                   const float *w, const void *w1, const float *s1, const void *w2,
+                                   const float *s2, int64_t T, int k, int E, int64_t C, int64_t F,
+                                   void *f, void *ws, size_t ws_bytes, mhc_stream_t stream);
 
 /* ------------------------------------------------------------------ */
 /* Per-kernel timing (off by default).  When enabled, every kernel the  */

@@ -36,6 +36,8 @@ __all__ = [
     "mhc_qk_norm_rope_fwd", "mhc_qk_norm_rope_bwd", "OP_QK_NORM_ROPE_BWD", "mhc_moe_router_fwd",
     "mhc_moe_router_bwd", "SCORE_SOFTMAX", "SCORE_SIGMOID", "mhc_moe_rows", "mhc_moe_sort",
     "mhc_moe_dispatch_fwd", "mhc_moe_dispatch_bwd", "mhc_moe_combine_fwd", "mhc_moe_combine_bwd",
+    "mhc_fp8_quant", "mhc_fp8_swiglu_fwd", "mhc_fp8_swiglu_bwd", "mhc_fp8_gemm", "mhc_fp8_wgrad",
+    "mhc_moe_few_fwd", "OP_MOE_FEW_FWD",
 ]
 
 

@@ -33,6 +33,7 @@ OP_COMPUTE_H_BWD = 10
 OP_PROJ_RMS_PARTIAL_BWD = 11
 OP_H_POST_BDA_COMPUTE_H_FWD = 12
 OP_QK_NORM_ROPE_BWD = 13
+OP_MOE_FEW_FWD = 14
 
 SCORE_SOFTMAX = 0
 SCORE_SIGMOID = 1
@@ -92,6 +93,12 @@ _SIGS = {
     "mhc_moe_dispatch_bwd": [_P, _I, _P, _I64, _I, _I64, _I64, _P, _P],
     "mhc_moe_combine_fwd": [_P, _I, _P, _P, _I64, _I, _I64, _I64, _P, _P],
     "mhc_moe_combine_bwd": [_P, _P, _I, _P, _P, _P, _I64, _I, _I64, _I64, _P, _P, _P],
+    "mhc_fp8_quant": [_P, _I, _I64, _I64, _I64, _I, _I, _P, _P, _P, _P, _P],
+    "mhc_fp8_swiglu_fwd": [_P, _I, _I64, _I64, _I, _P, _P, _P, _P, _P, _P],
+    "mhc_fp8_swiglu_bwd": [_P, _P, _I, _I64, _I64, _I, _P, _P, _P, _P, _P, _P],
+    "mhc_fp8_gemm": [_P, _I, _P, _P, _I, _P, _P, _I64, _I64, _I64, _I64, _I, _P, _P],
+    "mhc_fp8_wgrad": [_P, _I, _P, _P, _I, _P, _P, _I64, _I64, _I64, _I64, _I, _P, _P],
+    "mhc_moe_few_fwd": [_P, _I, _P, _P, _P, _P, _P, _P, _I64, _I, _I, _I64, _I64, _P, _P, _SZ, _P],
 }
 for _name, _args in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -490,9 +497,11 @@ def _load_marshal():
     loader.exec_module(m)
     entries = ("mhc_qk_norm_rope_fwd", "mhc_qk_norm_rope_bwd", "mhc_moe_router_fwd",
                "mhc_moe_router_bwd", "mhc_moe_sort", "mhc_moe_dispatch_fwd", "mhc_moe_dispatch_bwd",
-               "mhc_moe_combine_fwd", "mhc_moe_combine_bwd")
+               "mhc_moe_combine_fwd", "mhc_moe_combine_bwd", "mhc_fp8_quant", "mhc_fp8_swiglu_fwd",
+               "mhc_fp8_swiglu_bwd", "mhc_fp8_gemm", "mhc_fp8_wgrad", "mhc_moe_few_fwd")
     m.setup(torch.Tensor,
-            (torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8),
+            (torch.bfloat16, torch.float16, torch.float32, torch.int32, torch.uint8,
+             torch.float8_e4m3fn, torch.float8_e5m2),
             tuple(ctypes.cast(getattr(lib, n), _P).value for n in entries))
     return m
 
@@ -564,6 +573,35 @@ def mhc_moe_combine_fwd(ys, w, row_of, f, stream=None):
 
 def mhc_moe_combine_bwd(df, ys, w, row_of, slot_of, dys, dw=None, stream=None):
     _ok(_marshal.combine_bwd(df, ys, w, row_of, slot_of, dys, dw, _handle(stream)))
+
+
+def mhc_fp8_quant(x, q=None, s=None, qt=None, st=None, tiles=False, stream=None):
+    """x [R, C] or [G, R, C]; the format is q's (or qt's) dtype."""
+    _ok(_marshal.fp8_quant(x, q, s, qt, st, tiles, _handle(stream)))
+
+
+def mhc_fp8_swiglu_fwd(h, a=None, q=None, s=None, qt=None, st=None, stream=None):
+    _ok(_marshal.fp8_swiglu_fwd(h, a, q, s, qt, st, _handle(stream)))
+
+
+def mhc_fp8_swiglu_bwd(da, h, dh=None, q=None, s=None, qt=None, st=None, stream=None):
+    _ok(_marshal.fp8_swiglu_bwd(da, h, dh, q, s, qt, st, _handle(stream)))
+
+
+def mhc_fp8_gemm(a, sa, b, sb, offsets, out, stream=None):
+    """a [R, K], b [G, N, K], out [R, N]; offsets None: a plain product (G = 1)."""
+    _ok(_marshal.fp8_gemm(a, sa, b, sb, offsets, out, _handle(stream)))
+
+
+def mhc_fp8_wgrad(at, sat, bt, sbt, offsets, out, stream=None):
+    """at [M, R], bt [N, R], out [G, M, N]; offsets None: one segment (G = 1)."""
+    _ok(_marshal.fp8_wgrad(at, sat, bt, sbt, offsets, out, _handle(stream)))
+
+
+def mhc_moe_few_fwd(x, ids, w, w1, w2, f, ws, s1=None, s2=None, stream=None):
+    """x [T, C], w1 [E, 2F, C], w2 [E, C, F]; with s1, s2 the weights are
+    float8_e4m3fn.  ws: workspace(OP_MOE_FEW_FWD, T, k, C + F)."""
+    _ok(_marshal.few_fwd(x, ids, w, w1, w2, f, ws, s1, s2, _handle(stream)))
 
 
 def mhc_set_batch_invariant(on: bool) -> None:

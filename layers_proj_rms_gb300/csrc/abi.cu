@@ -8,6 +8,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "../../include/mhc.h"
+#include "fp8.h"
 #include "launch.h"
 #include "moe.h"
 #include "qk.h"
@@ -269,12 +270,18 @@ size_t mhc_workspace_bytes(mhc_op op, int64_t T, int n, int64_t C)
 {
     if (op == MHC_OP_QK_NORM_ROPE_BWD)  // n = Hq + Hk, C = D
         return T < 0 || n < 0 || C < 1 || C > MHC_MAX_HEAD_DIM ? 0 : mhc::qk_bwd_ws_bytes(T, n, C);
+    if (op == MHC_OP_MOE_FEW_FWD)  // n = k, C = C + F
+        return T < 0 || T > MHC_MOE_FEW_TOKENS || n < 1 || n > MHC_MOE_MAX_K || C < 32 || C % 16 ||
+                       C > 2 * MHC_MOE_FEW_MAX_C
+                   ? 0
+                   : mhc::moe_few_ws_bytes(T, n, C);
     if (T < 0 || C < 8 || C % 8 != 0) return 0;
     if (op == MHC_OP_RMSNORM_RESIDUAL_BWD) return mhc::norm_ws_bytes(T, C);  // n unused
     if (n != 4 && n != 8) return 0;
     switch (op) {
     case MHC_OP_RMSNORM_RESIDUAL_BWD: return 0;
     case MHC_OP_QK_NORM_ROPE_BWD: return 0;
+    case MHC_OP_MOE_FEW_FWD: return 0;
     case MHC_OP_H_AGGREGATE_RMSNORM_BWD: return mhc::norm_ws_bytes(T, C);
     case MHC_OP_H_AGGREGATE_STATIC_BWD: return mhc::agg_static_ws_bytes(T, n);
     case MHC_OP_PROJ_RMS_PARTIAL_FWD: return mhc::proj_fwd_ws_bytes(T, n, C);
@@ -1118,6 +1125,200 @@ mhc_status mhc_moe_combine_bwd(const void *df, const void *ys, mhc_dtype dtype, 
     if (ck.st) return ck.st;
     return launched(ck.fn, mhc::launch_moe_combine_bwd(df, ys, int(dtype), w, row_of, slot_of, T, k,
                                                        R, C, dys, dw, fault_ptr(), stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// the experts' products in 8-bit floating point
+// ---------------------------------------------------------------------------
+
+namespace {
+
+mhc_status format_ok(Check &ck, int f, const char *name)
+{
+    if (ck.st == MHC_OK && f != MHC_E4M3 && f != MHC_E5M2)
+        ck.st = fail(MHC_ERR_BAD_ARG, "%s: %s = %d is neither MHC_E4M3 nor MHC_E5M2", ck.fn, name, f);
+    return ck.st;
+}
+
+void multiple(Check &ck, int64_t v, int64_t of, const char *name)
+{
+    if (ck.st == MHC_OK && v % of)
+        ck.st = fail(MHC_ERR_BAD_SHAPE, "%s: %s = %lld must be a multiple of %lld", ck.fn, name,
+                     (long long)v, (long long)of);
+}
+
+// Sizes and outputs of a quantisation; x and da are checked by the caller.
+void quant_args(Check &ck, mhc::Fp8QuantArgs &a, int dtype, int format, int64_t G, int64_t R,
+                int64_t C, void *y, uint8_t *q, float *s, uint8_t *qt, float *st)
+{
+    ck.dtype(dtype).range(G, 0, 65535, "G").range(R, 0, INT32_MAX, "R");
+    ck.range(C, 16, int64_t(1) << 30, "C");
+    format_ok(ck, format, "format");
+    multiple(ck, C, 16, "C");
+    if (qt || st) multiple(ck, R, 16, "R");
+    if (ck.st == MHC_OK && mhc::fp8_blocks(R) * mhc::fp8_blocks(C) > INT32_MAX)
+        ck.st = fail(MHC_ERR_BAD_SHAPE, "%s: R and C give more than 2^31 tiles", ck.fn);
+    if (ck.st || G == 0 || R == 0) return;
+    if (q || s) ck.ptr(q, "q").ptr(s, "s");
+    if (qt || st) ck.ptr(qt, "qt").ptr(st, "st");
+    ck.opt(y, "the unquantised output");
+    if (ck.st == MHC_OK && !q && !qt && !y)
+        ck.st = fail(MHC_ERR_NULL_PTR, "%s: every output is NULL", ck.fn);
+    a.y = y;
+    a.q = q;
+    a.s = s;
+    a.qt = qt;
+    a.st = st;
+    a.G = G;
+    a.R = R;
+    a.C = C;
+    a.ncb = unsigned(mhc::fp8_blocks(C));
+}
+
+// Sizes of a grouped product with output tiles of mt x nt (out: M x N in each of `groups`).
+void group_args(Check &ck, int fa, int fb, const int32_t *offsets, int64_t G, int64_t R,
+                int out_dtype)
+{
+    format_ok(ck, fa, "format_a");
+    format_ok(ck, fb, "format_b");
+    ck.dtype(out_dtype).range(G, 1, MHC_MOE_MAX_EXPERTS, "G").range(R, 0, INT32_MAX, "R");
+    if (ck.st == MHC_OK && !offsets && G != 1)
+        ck.st = fail(MHC_ERR_NULL_PTR, "%s: offsets is NULL and G = %lld", ck.fn, (long long)G);
+    if (ck.st == MHC_OK && reinterpret_cast<uintptr_t>(offsets) % 4)
+        ck.st = fail(MHC_ERR_MISALIGNED, "%s: offsets is not 4-byte aligned", ck.fn);
+}
+
+void tiles_fit(Check &ck, int64_t a, int64_t b)
+{
+    if (ck.st == MHC_OK && a > 0 && b > INT32_MAX / a)
+        ck.st = fail(MHC_ERR_BAD_SHAPE, "%s: more than 2^31 output tiles", ck.fn);
+}
+
+}  // namespace
+
+extern "C" {
+
+mhc_status mhc_fp8_quant(const void *x, mhc_dtype dtype, int64_t G, int64_t R, int64_t C,
+                         mhc_fp8 format, int tiles, uint8_t *q, float *s, uint8_t *qt, float *st,
+                         mhc_stream_t stream)
+{
+    Check ck("mhc_fp8_quant");
+    mhc::Fp8QuantArgs a = {};
+    quant_args(ck, a, int(dtype), int(format), G, R, C, nullptr, q, s, qt, st);
+    if (ck.st || G == 0 || R == 0) return ck.st;
+    ck.ptr(x, "x").device();
+    if (ck.st) return ck.st;
+    a.x = x;
+    a.tiles = tiles != 0;
+    return launched(ck.fn, mhc::launch_fp8_quant(a, mhc::kFp8Plain, int(dtype), int(format), stream));
+}
+
+mhc_status mhc_fp8_swiglu_fwd(const void *h, mhc_dtype dtype, int64_t R, int64_t F, mhc_fp8 format,
+                              void *a, uint8_t *q, float *s, uint8_t *qt, float *st,
+                              mhc_stream_t stream)
+{
+    Check ck("mhc_fp8_swiglu_fwd");
+    mhc::Fp8QuantArgs g = {};
+    ck.range(F, 16, int64_t(1) << 29, "F");
+    multiple(ck, F, 16, "F");
+    quant_args(ck, g, int(dtype), int(format), 1, R, F, a, q, s, qt, st);
+    if (ck.st || R == 0) return ck.st;
+    ck.ptr(h, "h").device();
+    if (ck.st) return ck.st;
+    g.x = h;
+    g.F = F;
+    return launched(ck.fn, mhc::launch_fp8_quant(g, mhc::kFp8Swiglu, int(dtype), int(format), stream));
+}
+
+mhc_status mhc_fp8_swiglu_bwd(const void *da, const void *h, mhc_dtype dtype, int64_t R, int64_t F,
+                              mhc_fp8 format, void *dh, uint8_t *q, float *s, uint8_t *qt,
+                              float *st, mhc_stream_t stream)
+{
+    Check ck("mhc_fp8_swiglu_bwd");
+    mhc::Fp8QuantArgs g = {};
+    ck.range(F, 16, int64_t(1) << 29, "F");
+    multiple(ck, F, 16, "F");
+    quant_args(ck, g, int(dtype), int(format), 1, R, 2 * F, dh, q, s, qt, st);
+    if (ck.st || R == 0) return ck.st;
+    ck.ptr(da, "da").ptr(h, "h").device();
+    if (ck.st) return ck.st;
+    g.x = h;
+    g.da = da;
+    g.F = F;
+    return launched(ck.fn,
+                    mhc::launch_fp8_quant(g, mhc::kFp8SwigluGrad, int(dtype), int(format), stream));
+}
+
+mhc_status mhc_fp8_gemm(const uint8_t *a, mhc_fp8 format_a, const float *sa, const uint8_t *b,
+                        mhc_fp8 format_b, const float *sb, const int32_t *offsets, int64_t G,
+                        int64_t R, int64_t N, int64_t K, mhc_dtype out_dtype, void *out,
+                        mhc_stream_t stream)
+{
+    Check ck("mhc_fp8_gemm");
+    group_args(ck, int(format_a), int(format_b), offsets, G, R, int(out_dtype));
+    ck.range(N, 8, INT32_MAX, "N").range(K, 16, INT32_MAX - 127, "K");
+    multiple(ck, N, 8, "N");
+    multiple(ck, K, 16, "K");
+    tiles_fit(ck, R / 128 + G + 1, N / 128 + 1);
+    ck.fits(G * N, K, "G*N*K").fits(R, N, "R*N");
+    if (ck.st || R == 0) return ck.st;
+    ck.ptr(a, "a").ptr(sa, "sa").ptr(b, "b").ptr(sb, "sb").ptr(out, "out").device();
+    if (ck.st) return ck.st;
+    const mhc::Fp8GemmArgs g = {a, b, sa, sb, offsets, G, R, N, K, int(format_a), int(format_b), out,
+                                fault_ptr()};
+    return launched(ck.fn, mhc::launch_fp8_gemm(g, int(out_dtype), stream));
+}
+
+mhc_status mhc_fp8_wgrad(const uint8_t *at, mhc_fp8 format_a, const float *sat, const uint8_t *bt,
+                         mhc_fp8 format_b, const float *sbt, const int32_t *offsets, int64_t G,
+                         int64_t R, int64_t M, int64_t N, mhc_dtype out_dtype, void *out,
+                         mhc_stream_t stream)
+{
+    Check ck("mhc_fp8_wgrad");
+    group_args(ck, int(format_a), int(format_b), offsets, G, R, int(out_dtype));
+    ck.range(M, 1, INT32_MAX - 127, "M").range(N, 8, INT32_MAX - 255, "N");
+    multiple(ck, N, 8, "N");
+    multiple(ck, R, 16, "R");
+    tiles_fit(ck, (M / 128 + 1) * G, N / 128 + 1);
+    ck.fits(G * M, N, "G*M*N");
+    if (ck.st) return ck.st;
+    ck.ptr(out, "out");
+    if (ck.st == MHC_OK && R == 0) {  // every segment is empty
+        if (ck.device().st) return ck.st;
+        const size_t es = out_dtype == MHC_FP32 ? 4 : 2;
+        return launched(ck.fn, cudaMemsetAsync(out, 0, size_t(G * M) * size_t(N) * es, stream));
+    }
+    ck.ptr(at, "at").ptr(sat, "sat").ptr(bt, "bt").ptr(sbt, "sbt").device();
+    if (ck.st) return ck.st;
+    const mhc::Fp8WgradArgs g = {at, bt, sat, sbt, offsets, G, R, M, N, int(format_a), int(format_b),
+                                 out, fault_ptr()};
+    return launched(ck.fn, mhc::launch_fp8_wgrad(g, int(out_dtype), stream));
+}
+
+mhc_status mhc_moe_few_fwd(const void *x, mhc_dtype dtype, const int32_t *ids, const float *w,
+                           const void *w1, const float *s1, const void *w2, const float *s2,
+                           int64_t T, int k, int E, int64_t C, int64_t F, void *f, void *ws,
+                           size_t ws_bytes, mhc_stream_t stream)
+{
+    Check ck("mhc_moe_few_fwd");
+    if (dtype != MHC_BF16 && dtype != MHC_FP16)
+        ck.st = fail(MHC_ERR_BAD_ARG, "%s: dtype = %d is neither MHC_BF16 nor MHC_FP16", ck.fn,
+                     int(dtype));
+    ck.range(T, 0, MHC_MOE_FEW_TOKENS, "T").range(k, 1, MHC_MOE_MAX_K, "k");
+    ck.range(E, 1, MHC_MOE_MAX_EXPERTS, "E");
+    ck.range(C, 16, MHC_MOE_FEW_MAX_C, "C").range(F, 16, MHC_MOE_FEW_MAX_C, "F");
+    multiple(ck, C, 16, "C");
+    multiple(ck, F, 16, "F");
+    if (ck.st == MHC_OK && !s1 != !s2)
+        ck.st = fail(MHC_ERR_NULL_PTR, "%s: one of s1 and s2 is NULL", ck.fn);
+    if (ck.st || T == 0) return ck.st;
+    ck.ptr(x, "x").ptr(ids, "ids").ptr(w, "w").ptr(w1, "w1").ptr(w2, "w2").ptr(f, "f");
+    ck.opt(s1, "s1").opt(s2, "s2").ws(ws, ws_bytes, mhc::moe_few_ws_bytes(T, k, C + F)).device();
+    if (ck.st) return ck.st;
+    const mhc::MoeFewArgs a = {x, ids, w, w1, w2, s1, s2, T, C, F, k, E, f, ws, fault_ptr()};
+    return launched(ck.fn, mhc::launch_moe_few(a, int(dtype), s1 != nullptr, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,53 @@
+// Device helpers of the 8-bit floating-point operators: a block's scale, the
+// conversions, the gated activation.
+#pragma once
+
+#include "common.cuh"
+
+namespace mhc {
+
+constexpr uint32_t kLeastBits = 0x0d800000u;  // 2^-100, the least amax of a block
+
+// FMT 0: e4m3, 1: e5m2.  Round to nearest even, saturating; NaN stays NaN.
+template <int FMT>
+__device__ __forceinline__ uint32_t f8_cvt2(float lo, float hi)
+{
+    uint16_t r;
+    if constexpr (FMT == 0)
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+template <int FMT>
+__device__ __forceinline__ uint32_t f8_cvt4(float a, float b, float c, float d)
+{
+    return f8_cvt2<FMT>(a, b) | f8_cvt2<FMT>(c, d) << 16;
+}
+
+template <int FMT>
+__device__ __forceinline__ float f8_top()
+{
+    return FMT == 0 ? 448.f : 57344.f;
+}
+// A magnitude's bits: they are ordered as the magnitudes, inf and NaN above all numbers.
+__device__ __forceinline__ uint32_t f8_mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// Scale and multiplier of a block whose largest magnitude has these bits.
+template <int FMT>
+__device__ __forceinline__ float f8_scale(uint32_t amax)
+{
+    return amax < 0x7f800000u ? __fdiv_rn(__uint_as_float(amax), f8_top<FMT>())
+                              : __uint_as_float(0x7fc00000u);
+}
+template <int FMT>
+__device__ __forceinline__ float f8_up(uint32_t amax)
+{
+    return __fdiv_rn(f8_top<FMT>(), __uint_as_float(amax));
+}
+
+// 1 / (1 + exp(-g)): 0 where exp(-g) is inf.
+__device__ __forceinline__ float sigm(float g) { return __frcp_rn(1.f + __expf(-g)); }
+// g p for p = sigm(g), 0 at -inf
+__device__ __forceinline__ float silu(float g, float p) { return p == 0.f ? 0.f : g * p; }
+
+}  // namespace mhc

@@ -1,5 +1,6 @@
 /* Argument marshalling of the sub-layer edge operators (q/k norm + rotation,
- * router, sort, dispatch, combine) for the Python binding: checks the torch
+ * router, sort, dispatch, combine) and of the experts' products in 8-bit
+ * floating point for the Python binding: checks the torch
  * tensors it is given (type, dtype, shape, contiguity, device), takes their
  * device pointers and calls the library's C entry points.  It does what
  * _lib.py does for the other entry points, in C because these operators are
@@ -15,13 +16,14 @@
 
 #include "../../include/mhc.h"
 
-enum { BF16 = MHC_BF16, FP16 = MHC_FP16, FP32 = MHC_FP32, I32, U8, NTYPES };
+enum { BF16 = MHC_BF16, FP16 = MHC_FP16, FP32 = MHC_FP32, I32, U8, E4M3, E5M2, NTYPES };
 
 static PyObject *tensor_type, *dtypes[NTYPES];
 static PyObject *s_shape, *s_dtype, *s_is_cuda, *s_is_contiguous, *s_data_ptr, *s_stride;
 
 static const char *const type_names[NTYPES] = {"torch.bfloat16", "torch.float16", "torch.float32",
-                                               "torch.int32", "torch.uint8"};
+                                               "torch.int32", "torch.uint8",
+                                               "torch.float8_e4m3fn", "torch.float8_e5m2"};
 
 /* The entry points, in the order that setup() gets their addresses. */
 static struct {
@@ -34,6 +36,12 @@ static struct {
     __typeof__(&mhc_moe_dispatch_bwd) dispatch_bwd;
     __typeof__(&mhc_moe_combine_fwd) combine_fwd;
     __typeof__(&mhc_moe_combine_bwd) combine_bwd;
+    __typeof__(&mhc_fp8_quant) fp8_quant;
+    __typeof__(&mhc_fp8_swiglu_fwd) fp8_swiglu_fwd;
+    __typeof__(&mhc_fp8_swiglu_bwd) fp8_swiglu_bwd;
+    __typeof__(&mhc_fp8_gemm) fp8_gemm;
+    __typeof__(&mhc_fp8_wgrad) fp8_wgrad;
+    __typeof__(&mhc_moe_few_fwd) few_fwd;
 } fn;
 
 #define CALL(status, ...)                                             \
@@ -479,7 +487,187 @@ static PyObject *py_combine_bwd(PyObject *self, PyObject *const *a, Py_ssize_t n
     return PyLong_FromLong(status);
 }
 
-/* setup(torch.Tensor, (bf16, fp16, fp32, int32, uint8 dtypes), (entry points' addresses)) */
+/* A contiguous [G, a, b] tensor of this type, [a, b] where nd is 2; `opt`: may be None. */
+static int batch(Tensor *t, int code, int nd, int64_t G, int64_t a, int64_t b, int opt)
+{
+    if (nd == 2) return exact(t, code, 2, a, b, opt);
+    if (opt && !t->obj) return 1;
+    if (!given(t)) return 0;
+    if (t->code != code) return wrong_type(t, type_names[code]);
+    if (t->nd != 3 || t->d[0] != G || t->d[1] != a || t->d[2] != b) return wrong_shape(t, 3, G, a, b);
+    return contiguous(t);
+}
+
+/* An 8-bit matrix of nd dimensions; sets *format. */
+static int eight(Tensor *t, int nd, int *format)
+{
+    if (!given(t)) return 0;
+    if (t->code != E4M3 && t->code != E5M2) return wrong_type(t, "float8_e4m3fn or float8_e5m2");
+    *format = t->code == E5M2 ? MHC_E5M2 : MHC_E4M3;
+    if (t->nd != nd) PyErr_Format(PyExc_ValueError, "%s must have %d dimensions", t->name, nd);
+    return t->nd == nd;
+}
+
+static int64_t blocks(int64_t n) { return (n + 127) / 128; }
+
+/* q, s, qt, st of a quantisation of [G, R, C] ([R, C] where nd is 2). */
+typedef struct {
+    Tensor q, s, qt, st;
+    int format;
+} Quant;
+
+static int quantised(PyObject *const *a, Quant *x, int nd, int64_t G, int64_t R, int64_t C, int tiles)
+{
+    if (!look(a[0], "q", &x->q) || !look(a[1], "s", &x->s) || !look(a[2], "qt", &x->qt) ||
+        !look(a[3], "st", &x->st))
+        return 0;
+    x->format = MHC_E4M3;
+    const Tensor *one = x->q.obj ? &x->q : &x->qt;
+    if (one->obj && !eight((Tensor *)one, nd, &x->format)) return 0;
+    const int code = x->format == MHC_E5M2 ? E5M2 : E4M3;
+    return batch(&x->q, code, nd, G, R, C, 1) && batch(&x->qt, code, nd, G, C, R, 1) &&
+           batch(&x->s, FP32, nd, G, blocks(C), tiles ? blocks(R) : R, !x->q.obj) &&
+           batch(&x->st, FP32, nd, G, blocks(R), tiles ? blocks(C) : C, !x->qt.obj);
+}
+
+/* (x, q, s, qt, st, tiles, stream) -> status */
+static PyObject *py_fp8_quant(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    Tensor x;
+    Quant o;
+    int code, tiles, status;
+    mhc_stream_t s;
+    if (!nargs(n, 7) || !look(a[0], "x", &x) || !given(&x) || (tiles = PyObject_IsTrue(a[5])) < 0 ||
+        !activation(&x, x.nd == 3 ? 3 : 2, &code) || !contiguous(&x))
+        return NULL;
+    const int64_t G = x.nd == 3 ? x.d[0] : 1, R = x.d[x.nd - 2], C = x.d[x.nd - 1];
+    if (!quantised(a + 1, &o, x.nd, G, R, C, tiles) || !handle(a[6], &s)) return NULL;
+    CALL(status, fn.fp8_quant(x.ptr, (mhc_dtype)code, G, R, C, (mhc_fp8)o.format, tiles, o.q.ptr,
+                              o.s.ptr, o.qt.ptr, o.st.ptr, s))
+    return PyLong_FromLong(status);
+}
+
+/* h [R, 2F] */
+static int gate_up(Tensor *h, int *code)
+{
+    if (!activation(h, 2, code) || !contiguous(h)) return 0;
+    if (h->d[1] % 2) PyErr_Format(PyExc_ValueError, "h: its %lld columns are no two halves",
+                                  (long long)h->d[1]);
+    return h->d[1] % 2 == 0;
+}
+
+/* (h, a, q, s, qt, st, stream) -> status */
+static PyObject *py_fp8_swiglu_fwd(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    Tensor h, y;
+    Quant o;
+    int code, status;
+    mhc_stream_t s;
+    if (!nargs(n, 7) || !look(a[0], "h", &h) || !look(a[1], "a", &y) || !gate_up(&h, &code)) return NULL;
+    const int64_t R = h.d[0], F = h.d[1] / 2;
+    if (!exact(&y, code, 2, R, F, 1) || !quantised(a + 2, &o, 2, 1, R, F, 0) || !handle(a[6], &s))
+        return NULL;
+    CALL(status, fn.fp8_swiglu_fwd(h.ptr, (mhc_dtype)code, R, F, (mhc_fp8)o.format, y.ptr, o.q.ptr,
+                                   o.s.ptr, o.qt.ptr, o.st.ptr, s))
+    return PyLong_FromLong(status);
+}
+
+/* (da, h, dh, q, s, qt, st, stream) -> status */
+static PyObject *py_fp8_swiglu_bwd(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    Tensor da, h, y;
+    Quant o;
+    int code, status;
+    mhc_stream_t s;
+    if (!nargs(n, 8) || !look(a[0], "da", &da) || !look(a[1], "h", &h) || !look(a[2], "dh", &y) ||
+        !gate_up(&h, &code))
+        return NULL;
+    const int64_t R = h.d[0], F = h.d[1] / 2;
+    if (!exact(&da, code, 2, R, F, 0) || !exact(&y, code, 2, R, 2 * F, 1) ||
+        !quantised(a + 3, &o, 2, 1, R, 2 * F, 0) || !handle(a[7], &s))
+        return NULL;
+    CALL(status, fn.fp8_swiglu_bwd(da.ptr, h.ptr, (mhc_dtype)code, R, F, (mhc_fp8)o.format, y.ptr,
+                                   o.q.ptr, o.s.ptr, o.qt.ptr, o.st.ptr, s))
+    return PyLong_FromLong(status);
+}
+
+/* (a, sa, b, sb, offsets, out, stream) -> status */
+static PyObject *py_fp8_gemm(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    Tensor x, sx, w, sw, off, out;
+    int fa, fb, code, status;
+    mhc_stream_t s;
+    if (!nargs(n, 7) || !look(a[0], "a", &x) || !look(a[1], "sa", &sx) || !look(a[2], "b", &w) ||
+        !look(a[3], "sb", &sw) || !look(a[4], "offsets", &off) || !look(a[5], "out", &out) ||
+        !eight(&x, 2, &fa) || !eight(&w, 3, &fb) || !activation(&out, 2, &code) || !contiguous(&x) ||
+        !contiguous(&w))
+        return NULL;
+    const int64_t R = x.d[0], K = x.d[1], G = w.d[0], N = w.d[1];
+    if (!batch(&w, w.code, 3, G, N, K, 0) || !exact(&sx, FP32, 2, blocks(K), R, 0) ||
+        !batch(&sw, FP32, 3, G, blocks(K), blocks(N), 0) || !exact(&off, I32, 1, G + 1, 0, 1) ||
+        !exact(&out, code, 2, R, N, 0) || !handle(a[6], &s))
+        return NULL;
+    CALL(status, fn.fp8_gemm(x.ptr, (mhc_fp8)fa, sx.ptr, w.ptr, (mhc_fp8)fb, sw.ptr, off.ptr, G, R, N,
+                             K, (mhc_dtype)code, out.ptr, s))
+    return PyLong_FromLong(status);
+}
+
+/* (at, sat, bt, sbt, offsets, out, stream) -> status */
+static PyObject *py_fp8_wgrad(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    Tensor x, sx, w, sw, off, out;
+    int fa, fb, code, status;
+    mhc_stream_t s;
+    if (!nargs(n, 7) || !look(a[0], "at", &x) || !look(a[1], "sat", &sx) || !look(a[2], "bt", &w) ||
+        !look(a[3], "sbt", &sw) || !look(a[4], "offsets", &off) || !look(a[5], "out", &out) ||
+        !eight(&x, 2, &fa) || !eight(&w, 2, &fb) || !activation(&out, 3, &code) || !contiguous(&x))
+        return NULL;
+    const int64_t M = x.d[0], R = x.d[1], G = out.d[0], N = w.d[0];
+    if (!exact(&w, w.code, 2, N, R, 0) || !exact(&sx, FP32, 2, blocks(R), M, 0) ||
+        !exact(&sw, FP32, 2, blocks(R), N, 0) || !exact(&off, I32, 1, G + 1, 0, 1) ||
+        !batch(&out, code, 3, G, M, N, 0) || !handle(a[6], &s))
+        return NULL;
+    CALL(status, fn.fp8_wgrad(x.ptr, (mhc_fp8)fa, sx.ptr, w.ptr, (mhc_fp8)fb, sw.ptr, off.ptr, G, R, M,
+                              N, (mhc_dtype)code, out.ptr, s))
+    return PyLong_FromLong(status);
+}
+
+/* (x, ids, w, w1, w2, f, ws, s1, s2, stream) -> status */
+static PyObject *py_few_fwd(PyObject *self, PyObject *const *a, Py_ssize_t n)
+{
+    (void)self;
+    Tensor x, ids, w, w1, w2, f, ws, s1, s2;
+    int code, status;
+    mhc_stream_t s;
+    if (!nargs(n, 10) || !look(a[0], "x", &x) || !look(a[1], "ids", &ids) || !look(a[2], "w", &w) ||
+        !look(a[3], "w1", &w1) || !look(a[4], "w2", &w2) || !look(a[5], "f", &f) ||
+        !look(a[6], "ws", &ws) || !look(a[7], "s1", &s1) || !look(a[8], "s2", &s2) ||
+        !activation(&x, 2, &code) || !contiguous(&x) || !matrix(&ids) || !given(&w1) || !given(&w2))
+        return NULL;
+    const int64_t T = x.d[0], C = x.d[1], k = ids.d[1];
+    if (w2.nd != 3) {
+        PyErr_SetString(PyExc_ValueError, "w2 must have 3 dimensions");
+        return NULL;
+    }
+    const int64_t E = w2.d[0], F = w2.d[2];
+    const int wc = s1.obj || s2.obj ? E4M3 : code;
+    if (!exact(&ids, I32, 2, T, k, 0) || !exact(&w, FP32, 2, T, k, 0) ||
+        !batch(&w1, wc, 3, E, 2 * F, C, 0) || !batch(&w2, wc, 3, E, C, F, 0) ||
+        !batch(&s1, FP32, 3, E, blocks(C), blocks(2 * F), wc != E4M3) ||
+        !batch(&s2, FP32, 3, E, blocks(F), blocks(C), wc != E4M3) || !exact(&f, code, 2, T, C, 0) ||
+        !exact(&ws, U8, 1, ws.numel, 0, 1) || !handle(a[9], &s) || !small(k, "k") || !small(E, "E"))
+        return NULL;
+    CALL(status, fn.few_fwd(x.ptr, (mhc_dtype)code, ids.ptr, w.ptr, w1.ptr, s1.ptr, w2.ptr, s2.ptr, T,
+                            (int)k, (int)E, C, F, f.ptr, ws.ptr, (size_t)ws.numel, s))
+    return PyLong_FromLong(status);
+}
+
+/* setup(torch.Tensor, (the dtypes in the order of type_names), (entry points' addresses)) */
 static PyObject *py_setup(PyObject *self, PyObject *args)
 {
     (void)self;
@@ -511,6 +699,8 @@ static PyMethodDef methods[] = {
     {"setup", py_setup, METH_VARARGS, NULL},
     ENTRY(qk_fwd), ENTRY(qk_bwd), ENTRY(router_fwd), ENTRY(router_bwd), ENTRY(sort),
     ENTRY(dispatch_fwd), ENTRY(dispatch_bwd), ENTRY(combine_fwd), ENTRY(combine_bwd),
+    ENTRY(fp8_quant), ENTRY(fp8_swiglu_fwd), ENTRY(fp8_swiglu_bwd), ENTRY(fp8_gemm),
+    ENTRY(fp8_wgrad), ENTRY(few_fwd),
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", NULL, -1, methods,

@@ -46,6 +46,13 @@ bool tmap_bf16(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
     return tmap_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, rank, dims, strides_bytes, box, sw);
 }
 
+bool tmap_u8(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
+             const uint64_t *strides_bytes, const uint32_t *box)
+{
+    return tmap_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, rank, dims, strides_bytes, box,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 bool tmap_f32_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                  uint32_t box_cols, CUtensorMapSwizzle sw)
 {

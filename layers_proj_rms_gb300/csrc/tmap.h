@@ -1,4 +1,4 @@
-// TMA tensor maps of bf16 and fp32 tensors for the tensor-core kernels (the driver's
+// TMA tensor maps of bf16, fp32 and 8-bit tensors for the tensor-core kernels (the driver's
 // cuTensorMapEncodeTiled, looked up once through the runtime).
 #pragma once
 
@@ -22,6 +22,10 @@ inline bool tmap_bf16_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64
     const uint32_t box[2] = {box_cols, box_rows};
     return tmap_bf16(m, base, 2, dims, strides, box, sw);
 }
+
+// A `rank`-dimensional tensor of bytes in the 128-byte swizzle.
+bool tmap_u8(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
+             const uint64_t *strides_bytes, const uint32_t *box);
 
 // A row-major [rows][cols] fp32 matrix, box [box_rows][box_cols].
 bool tmap_f32_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows,
