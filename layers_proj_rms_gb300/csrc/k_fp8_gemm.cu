@@ -14,12 +14,26 @@
 // registers, so scales of any value are exact to fp32 and the long sum is
 // rounded to nearest, once a block.
 //
-// A CTA is persistent, one an SM: a TMA producer, the MMA issuer, a warp that
-// brings the scales (cp.async, as deep as the tiles' ring), a spare warp and
-// eight epilogue warps, each 32 rows x half the columns.
+// What bounds it: one CTA's MMA of 128 x 256 x 32 reads 12 KB of shared memory
+// and its TMA loads write as much, 1.5 times what the SM can do while the MMA
+// runs (measured: 855 cycles a block of 128, of 512 for the products).  So two
+// CTAs share a tile of 256 x 256 (cta_group::2), each with its 128 rows of A and
+// half of B: 32 KB in and 32 KB out for the same 512 cycles.  Where the segments
+// are short (below 160 rows on average a pair would work on empty rows) a CTA
+// takes tiles of 128 x 128 by itself: there the weights' way through HBM is what
+// counts, and a stage is 32 KB all the same.
+//
+// A CTA is persistent, one an SM: a warp that brings the operands (TMA) and the
+// scales (cp.async), two that issue the MMAs of the even and the odd blocks (the
+// first CTA's of a pair), one that waits for them, and eight epilogue warps, in a
+// pair sixteen, each 32 rows x 64 columns.  Results leave
+// through a 4 KB box of shared memory a warp (32 rows x 128 bytes) by TMA store, so
+// the next tile's blocks do not wait for them; a box that the segment's end cuts
+// is copied row by row.
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "elem.cuh"
 #include "fp8.h"
@@ -36,25 +50,29 @@ constexpr int BM = 128, BK = 128;
 // Fault codes of bad offsets in device memory.
 enum : int { kFaultOffsets = 205, kFaultOffsetsAlign = 206 };
 
-template <int BN_>
+// CG CTAs share a tile of 128 CG x BN; each loads 128 rows of A and of B a block.
+template <int CG_, int BN_>
 struct GemmCfg {
-    static constexpr int BN = BN_;
-    static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = BN == 256 ? 4 : 6;
-    static constexpr int SC = 5;  // blocks whose scales are in flight
+    static constexpr int CG = CG_, BN = BN_;
+    static_assert(BN == 128 * CG, "each CTA loads 128 rows of B");
+    static constexpr int A_BYTES = BM * BK, B_BYTES = 128 * BK, STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = 4;
+    static constexpr int SC = 6;     // blocks whose scales are there or in flight
+    static constexpr int AHEAD = 4;  // of them in flight at most; two are being read
     static constexpr int SC_FLOATS = BM + BN;
-    static constexpr int EPI_WARPS = 8;
-    static constexpr int HALF = BN / 2;  // columns of an epilogue warp
-    static constexpr int OUT_BYTES = EPI_WARPS * 32 * 64;
+    static constexpr int COLS = 64;  // of an epilogue warp
+    static constexpr int GROUPS = BN / COLS;  // of four epilogue warps
+    static constexpr int EPI_WARPS = 4 * GROUPS;
+    static constexpr int BOX = 32 * 128;
     static constexpr int THREADS = 32 * (4 + EPI_WARPS);
     static constexpr int TMEM_COLS = 2 * BN;
-    // shared memory: stages, output staging, scales, segments' starts and first tiles, barriers
+    // shared memory: stages, output boxes, scales, segments' starts and first tiles, barriers
     static constexpr int OFF_OUT = STAGES * STAGE;
-    static constexpr int OFF_SC = OFF_OUT + OUT_BYTES;
+    static constexpr int OFF_SC = OFF_OUT + EPI_WARPS * BOX;
     static constexpr int OFF_SEG = OFF_SC + SC * SC_FLOATS * 4;
     static constexpr int OFF_TILE = OFF_SEG + 1040 * 4;
     static constexpr int OFF_BAR = OFF_TILE + 1040 * 4;
-    static constexpr int SMEM = OFF_BAR + 512 + 1024 /*align*/;
+    static constexpr int SMEM = OFF_BAR + 256 + 1024 /*align*/;
     static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -65,25 +83,160 @@ struct GemmP {
     int64_t N;
     int G, R;            // segments, sorted rows
     int nkb;             // rows: blocks of K
-    int mt, nt;          // tiles of M (weights) and N
+    int mt, nt;          // tiles of M (weights) and N, of a pair where there are two CTAs
     uint32_t idesc;
     void *out;
     int *fault;
 };
 
+template <int CG>
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                        uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile(
-        "{\n"
-        ".reg .pred p;\n"
-        "setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-        "}\n" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "setp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+            "}\n" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "setp.ne.b32 p, %4, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+            "}\n" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
 }
 
+// Arrives on `bar`, in a pair on both CTAs' barriers at that place, when all
+// earlier MMAs of this thread are complete.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    if constexpr (CG == 1)
+        tc::mma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+            " [%0], %1;" ::"r"(tc::smem_u32(bar)),
+            "h"(uint16_t(3))
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols)
+{
+    if constexpr (CG == 1) {
+        tc::tmem_alloc(dst, ncols);
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         tc::smem_u32(dst)),
+                     "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+template <int CG>
+__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols)
+{
+    if constexpr (CG == 1)
+        tc::tmem_dealloc(taddr, ncols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                     : "memory");
+}
+
+__device__ __forceinline__ uint32_t cta_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// The shared::cluster address of the first CTA's copy of what stands at p here.
+__device__ __forceinline__ uint32_t of_first(const void *p)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(tc::smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// An arrival on a barrier of the first CTA.  What it orders is reads of TMEM, which
+// have ended before it (tcgen05.wait::ld), no writes to memory: with a release at
+// cluster scope, a fence of all the warp's memory operations, the epilogue took 1680
+// cycles a block, of 500.
+__device__ __forceinline__ void arrive_first(const uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(of_first(bar)) : "memory");
+}
+
+// Named barriers: block i's products are there (a group of epilogue warps and the
+// warp that waits for them), block i's accumulator is read (all epilogue warps and
+// the MMA warp); i even or odd.
+__device__ __forceinline__ int bar_ready(int group, int b) { return 1 + 2 * group + b; }
+__device__ __forceinline__ int bar_read(int b) { return 9 + b; }
+__device__ __forceinline__ void bar_arrive(int id, int count)
+{
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// TMA loads into this CTA's shared memory; a pair's complete on a barrier of the first CTA.
+template <int CG>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar)
+{
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+}
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *m, int x, int y, int z,
+                                        uint32_t bar)
+{
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+}
+
+__device__ __forceinline__ void store_2d(const CUtensorMap *m, uint32_t src, int x, int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void store_3d(const CUtensorMap *m, uint32_t src, int x, int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
 // Instruction descriptor of kind::f8f6f4, K-major A and B in 8 bits (0 e4m3,
 // 1 e5m2), fp32 accumulator, shape M x N.
 constexpr uint32_t idesc_f8_f32(int fa, int fb, int M, int N)
@@ -92,31 +245,30 @@ constexpr uint32_t idesc_f8_f32(int fa, int fb, int M, int N)
            (uint32_t(M >> 4) << 24);
 }
 
-// Arrives on `bar` when this thread's earlier cp.async copies have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar)
+// 16 consecutive TMEM columns.  The registers hold them once tmem_wait() is
+// through; what uses them also uses a value that passes through that wait, so it
+// cannot be moved before it.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
 {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(tc::smem_u32(bar))
-                 : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(taddr));
 }
-
-// 32 consecutive TMEM columns, as 16 pairs.
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t taddr, f32x2 (&v)[16])
+// 16 TMEM lanes x 32 columns as fragments: v[4 j + 2 i + c] is lane 8 i + lane / 4,
+// column 8 j + 2 (lane % 4) + c.
+__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, float (&v)[16])
 {
-    uint32_t r[32];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-          "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        v[i] = f2_make(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait(float &through)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(through)::"memory");
+}
+__device__ __forceinline__ void tmem_wait(float &through, float &too)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+f"(through), "+f"(too)::"memory");
 }
 
 // One output tile: where its operands and results stand.
@@ -131,7 +283,8 @@ struct Tile {
 // Tiles of an expert go down the rows first, in groups of 16 row tiles: the
 // CTAs that run at one time then share both operands' tiles in L2.
 template <class P, bool W>
-__device__ __forceinline__ Tile tile_of(const GemmP &p, const int *seg, const int *first, int t)
+__device__ __forceinline__ Tile tile_of(const GemmP &p, const int *seg, const int *first, int t,
+                                        int rank)
 {
     Tile x;
     int local, mt;
@@ -157,12 +310,12 @@ __device__ __forceinline__ Tile tile_of(const GemmP &p, const int *seg, const in
     const int m = 16 * g + rem % ms;
     x.n0 = rem / ms * P::BN;
     if (W) {
-        x.row0 = m * BM;
+        x.row0 = (m * P::CG + rank) * BM;
         x.row_end = int(p.out_rows);
         x.kb0 = seg[x.e] / BK;
         x.nkb = (seg[x.e + 1] - seg[x.e] + BK - 1) / BK;
     } else {
-        x.row0 = seg[x.e] + m * BM;
+        x.row0 = seg[x.e] + (m * P::CG + rank) * BM;
         x.row_end = seg[x.e + 1];
         x.kb0 = 0;
         x.nkb = p.nkb;
@@ -170,11 +323,98 @@ __device__ __forceinline__ Tile tile_of(const GemmP &p, const int *seg, const in
     return x;
 }
 
+// Its number of blocks alone.
+template <bool W>
+__device__ __forceinline__ int blocks_of(const GemmP &p, const int *seg, int t)
+{
+    if (!W) return p.nkb;
+    const int e = t / (p.mt * p.nt);
+    return (seg[e + 1] - seg[e] + BK - 1) / BK;
+}
+
+// The scales of a CTA's blocks, one block after the other, by a warp: a lane's
+// pointers and what of them is inside, stepped from block to block.
+template <class P, bool W>
+struct Cursor {
+    static constexpr int NC = W ? P::BN / 128 : 1;  // copies of column scales
+    const float *row, *col;  // the lane's first row scale, its first column scale
+    int64_t row_step, col_step;
+    uint32_t in;   // bits 0-3: rows j*32 + lane; 4: all rows, 16 bytes a lane; 8..: columns
+    int t, tstep, ntiles, left;  // tile; blocks of it that are left, 0 at the end
+
+    __device__ __forceinline__ Cursor(const GemmP &p, const int *seg, const int *first, int t0,
+                                      int step, int nt, int rank, int lane)
+        : row(nullptr), col(nullptr), row_step(0), col_step(0), in(0), t(t0 - step), tstep(step),
+          ntiles(nt), left(1)
+    {
+        next(p, seg, first, rank, lane);
+    }
+    __device__ __forceinline__ void next(const GemmP &p, const int *seg, const int *first, int rank,
+                                         int lane)
+    {
+        row += row_step;
+        col += col_step;
+        if (--left) return;
+        do {
+            t += tstep;
+            if (t >= ntiles) return;
+            const Tile x = tile_of<P, W>(p, seg, first, t, rank);
+            left = x.nkb;
+            const int64_t r0 = int64_t(x.kb0) * p.out_rows + x.row0;
+            // all 128 rows by 16 bytes a lane, where they and the step are so aligned
+            const bool wide = x.row0 + BM <= x.row_end && ((r0 | p.out_rows) & 3) == 0;
+            in = wide ? 16u : 0u;
+#pragma unroll
+            for (int j = 0; j < BM / 32; ++j)
+                if (x.row0 + j * 32 + lane < x.row_end) in |= 1u << j;
+            row = p.sa + r0 + (wide ? 4 * lane : lane);
+            row_step = p.out_rows;
+            if (W) {
+                // N is a multiple of 8: four columns are in or out together
+                col = p.sb + int64_t(x.kb0) * p.N + x.n0 + 4 * lane;
+                col_step = p.N;
+#pragma unroll
+                for (int j = 0; j < NC; ++j)
+                    if (x.n0 + j * 128 + 4 * lane < p.N) in |= 256u << j;
+            } else {
+                const int nbs = int((p.N + 127) / 128), nb = x.n0 / 128 + lane;
+                col = p.sb + int64_t(x.e) * p.nkb * nbs + nb;
+                col_step = nbs;
+                if (lane < P::BN / 128 && nb < nbs) in |= 256u;
+            }
+        } while (left == 0);
+    }
+    // brings the block's scales to dst (BM row scales, then the columns'); one group
+    __device__ __forceinline__ void load(const GemmP &p, uint32_t dst) const
+    {
+        const int lane = threadIdx.x & 31;
+        if (in & 16u) {
+            tc::cp_async16(dst + lane * 16, row, 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < BM / 32; ++j)
+                tc::cp_async4(dst + (j * 32 + lane) * 4, in >> j & 1 ? row + j * 32 : p.sa,
+                              in >> j & 1 ? 4 : 0);
+        }
+        if (W) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const bool on = in >> (8 + j) & 1;
+                tc::cp_async16(dst + (BM + j * 128 + 4 * lane) * 4, on ? col + j * 128 : p.sb, on ? 16 : 0);
+            }
+        } else if (lane < P::BN / 128) {
+            tc::cp_async4(dst + (BM + lane) * 4, in & 256u ? col : p.sb, in & 256u ? 4 : 0);
+        }
+        tc::cp_async_commit();
+    }
+};
+
 template <class P, bool W, class O>
 __global__ void __launch_bounds__(P::THREADS, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
-               const GemmP p)
+               const __grid_constant__ CUtensorMap tmo, const GemmP p)
 {
+    constexpr int CG = P::CG;
     pdl_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -184,35 +424,31 @@ __global__ void __launch_bounds__(P::THREADS, 1)
     int *first = reinterpret_cast<int *>(smem + P::OFF_TILE);
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR);
     uint64_t *empty = full + P::STAGES;
-    uint64_t *sc_full = empty + P::STAGES;
-    uint64_t *sc_empty = sc_full + P::SC;
-    uint64_t *acc_full = sc_empty + P::SC;
+    uint64_t *acc_full = empty + P::STAGES;
     uint64_t *acc_empty = acc_full + 2;
-    uint64_t *done = acc_empty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    volatile int *collected = abort_flag + 1;  // [2] even, odd blocks: one past the last one read
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 1 ? 0 : int(cta_rank());
     if (threadIdx.x == 0) {
         for (int s = 0; s < P::STAGES; ++s) {
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < P::SC; ++s) {
-            tc::mbar_init(&sc_full[s], 32);
-            tc::mbar_init(&sc_empty[s], P::EPI_WARPS);
-        }
         for (int b = 0; b < 2; ++b) {
             tc::mbar_init(&acc_full[b], 1);
-            tc::mbar_init(&acc_empty[b], P::EPI_WARPS);
+            tc::mbar_init(&acc_empty[b], 1);
         }
-        tc::mbar_init(done, 1);
         *abort_flag = 0;
+        collected[0] = collected[1] = 0;
         tc::fence_barrier_init();
         tc::tma_prefetch_desc(&tma);
         tc::tma_prefetch_desc(&tmb);
+        tc::tma_prefetch_desc(&tmo);
     }
-    if (warp == 1) tc::tmem_alloc(tmem_slot, P::TMEM_COLS);
+    if (warp == 1) tmem_alloc<CG>(tmem_slot, P::TMEM_COLS);
     // The segments: offsets that go back, leave the rows or (weights) stand off
     // the blocks are moved to the nearest that do not, and reported.
     for (int e = threadIdx.x; e <= p.G; e += P::THREADS)
@@ -240,7 +476,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
             // row tiles of segment e - 1 before v
             int prev = __shfl_up_sync(kFull, v, 1);
             if (lane == 0) prev = e0 == 0 ? v : carry;
-            int n = e <= p.G && e > 0 ? (v - prev + BM - 1) / BM : 0;
+            int n = e <= p.G && e > 0 ? (v - prev + CG * BM - 1) / (CG * BM) : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(kFull, n, d);
@@ -254,206 +490,314 @@ __global__ void __launch_bounds__(P::THREADS, 1)
     }
     tc::tc_fence_before();
     __syncthreads();
+    if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers are there
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int ntiles = W ? p.G * p.mt * p.nt : first[p.G] * p.nt;
-    // rows before the first segment belong to none
-    const int row_first = seg[0], row_last = seg[p.G];
+    const int t0 = blockIdx.x / CG, tstep = gridDim.x / CG;
 
-    // Registers go from the four issuing warps to the epilogue, which holds the
-    // sums: 128 * 56 + 256 * 224 = 384 * 168, what the block was launched with.
+    // In a pair registers go from the four issuing warps to the epilogue, which
+    // holds the sums: 128 * 64 + 512 * 104 = 640 * 96, what the block was launched with.
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-    if (warp == 0) {
-        if (lane == 0) {
-            int i = 0;
-            for (int t = blockIdx.x; t < ntiles && !*abort_flag; t += gridDim.x) {
-                const Tile x = tile_of<P, W>(p, seg, first, t);
-                for (int kb = 0; kb < x.nkb; ++kb, ++i) {
-                    const int s = i % P::STAGES;
-                    if (*abort_flag ||
-                        (i >= P::STAGES && !tc::mbar_wait(&empty[s], ((i / P::STAGES) & 1) ^ 1,
-                                                          p.fault, tc::kFaultTimeoutEmpty))) {
-                        *abort_flag = 1;
-                        break;
+        if constexpr (CG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // These loops run beside the epilogue's warps, at five cycles and more an
+        // instruction: a hundred instructions a block would be the products' time, so
+        // what changes from block to block is stepped, not computed.
+        if (warp == 0) {
+            if (lane == 0) {
+                int st = 0, left = 0;  // stage; loads that nothing has waited for
+                uint32_t ph = 1;       // a barrier's phase before its first counts as complete
+                const uint32_t smem0 = tc::smem_u32(smem), bar0 = tc::smem_u32(full);
+                const uint32_t to0 = CG == 1 ? bar0 : of_first(full);
+                bool ok = true;
+                for (int t = t0; t < ntiles && ok; t += tstep) {
+                    const Tile x = tile_of<P, W>(p, seg, first, t, rank);
+                    const int brow = x.n0 + rank * 128;
+                    int k = x.kb0 * BK;
+                    for (int kb = 0; kb < x.nkb; ++kb, k += BK) {
+                        ok = tc::mbar_wait(&empty[st], ph, p.fault, tc::kFaultTimeoutEmpty);
+                        if (!ok) break;
+                        const uint32_t a = smem0 + st * P::STAGE, bar = to0 + st * 8;
+                        if (rank == 0) tc::mbar_arrive_expect_tx(&full[st], CG * P::STAGE);
+                        load_2d<CG>(a, &tma, k, x.row0, bar);
+                        if (W)
+                            load_2d<CG>(a + P::A_BYTES, &tmb, k, brow, bar);
+                        else
+                            load_3d<CG>(a + P::A_BYTES, &tmb, k, brow, x.e, bar);
+                        left = min(left + 1, P::STAGES);
+                        if (++st == P::STAGES) {
+                            st = 0;
+                            ph ^= 1;
+                        }
                     }
-                    uint8_t *st = smem + s * P::STAGE;
-                    const int k = (x.kb0 + kb) * BK;
-                    tc::mbar_arrive_expect_tx(&full[s], P::STAGE);
-                    tc::tma_load_2d(st, &tma, k, x.row0, &full[s]);
-                    if (W)
-                        tc::tma_load_2d(st + P::A_BYTES, &tmb, k, x.n0, &full[s]);
-                    else
-                        tc::tma_load_3d(st + P::A_BYTES, &tmb, k, x.n0, x.e, &full[s]);
                 }
-            }
-            // do not leave while copies into this CTA's shared memory are in flight
-            for (int j = max(0, i - P::STAGES); j < i; ++j)
-                tc::mbar_wait(&full[j % P::STAGES], (j / P::STAGES) & 1, p.fault,
-                              tc::kFaultTimeoutMisc);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
-            int i = 0;
-            for (int t = blockIdx.x; t < ntiles && !*abort_flag; t += gridDim.x) {
-                const Tile x = tile_of<P, W>(p, seg, first, t);
-                for (int kb = 0; kb < x.nkb; ++kb, ++i) {
-                    const int s = i % P::STAGES, b = i & 1;
-                    if (*abort_flag ||
-                        !tc::mbar_wait(&full[s], (i / P::STAGES) & 1, p.fault,
-                                       tc::kFaultTimeoutFull) ||
-                        (i >= 2 && !tc::mbar_wait(&acc_empty[b], ((i >> 1) & 1) ^ 1, p.fault,
-                                                  tc::kFaultTimeoutAcc))) {
-                        *abort_flag = 1;
-                        break;
-                    }
-                    tc::tc_fence_after();
-                    const uint32_t a = tc::smem_u32(smem + s * P::STAGE);
-#pragma unroll
-                    for (int kk = 0; kk < BK / 32; ++kk)
-                        mma_f8(tmem + b * P::BN, tc::desc_kmajor_sw128(a + kk * 32),
-                               tc::desc_kmajor_sw128(a + P::A_BYTES + kk * 32), p.idesc, kk > 0);
-                    tc::mma_commit(&empty[s]);
-                    tc::mma_commit(&acc_full[b]);
+                // Do not leave while copies into this CTA's shared memory, MMAs that read it or
+                // their arrivals are in flight: what was issued is consumed.  After a fault that
+                // does not come; the copies then get the time that they may take.
+                for (; left > 0 && ok; --left) {
+                    // the oldest of the loads left: `left` stages back
+                    const int o = st - left;
+                    ok = tc::mbar_wait(&empty[o < 0 ? o + P::STAGES : o], o < 0 ? ph : ph ^ 1, p.fault,
+                                       tc::kFaultTimeoutMisc);
                 }
-            }
-            // the MMAs in flight end before TMEM and shared memory go
-            tc::mma_commit(done);
-            tc::mbar_wait(done, 0, p.fault, tc::kFaultTimeoutMisc);
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        int i = 0;
-        for (int t = blockIdx.x; t < ntiles && !*abort_flag; t += gridDim.x) {
-            const Tile x = tile_of<P, W>(p, seg, first, t);
-            for (int kb = 0; kb < x.nkb; ++kb, ++i) {
-                const int s = i % P::SC;
-                if (*abort_flag || (i >= P::SC && !tc::mbar_wait(&sc_empty[s], ((i / P::SC) & 1) ^ 1,
-                                                                 p.fault, tc::kFaultTimeoutEmpty))) {
+                if (!ok) {
                     *abort_flag = 1;
-                    break;
-                }
-                const uint32_t dst = tc::smem_u32(scales + s * P::SC_FLOATS);
-                const int64_t blk = x.kb0 + kb;
-                const float *ra = p.sa + blk * p.out_rows + x.row0;
-#pragma unroll
-                for (int j = 0; j < BM / 32; ++j) {
-                    const int r = j * 32 + lane;
-                    const bool in = x.row0 + r < x.row_end;
-                    tc::cp_async4(dst + r * 4, in ? ra + r : p.sa, in ? 4 : 0);
-                }
-                if (W) {
-                    const float *cb = p.sb + blk * p.N + x.n0;
-#pragma unroll
-                    for (int j = 0; j < P::BN / 32; ++j) {
-                        const int c = j * 32 + lane;
-                        const bool in = x.n0 + c < p.N;
-                        tc::cp_async4(dst + (BM + c) * 4, in ? cb + c : p.sb, in ? 4 : 0);
+                    const long long c0 = clock64();
+                    while (clock64() - c0 < 1000000) {
                     }
-                } else if (lane < (P::BN + 127) / 128) {
-                    const int nbs = int((p.N + 127) / 128), nb = x.n0 / 128 + lane;
-                    const bool in = nb < nbs;
-                    const float *cb = p.sb + (int64_t(x.e) * p.nkb + kb) * nbs + nb;
-                    tc::cp_async4(dst + (BM + lane) * 4, in ? cb : p.sb, in ? 4 : 0);
                 }
-                cp_async_arrive(&sc_full[s]);
             }
-        }
-        tc::cp_async_wait_all();
-        __syncwarp();
-        }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        const int q = warp & 3, h = (warp - 4) >> 2;
-        const uint32_t trow = tmem + (uint32_t(q * 32) << 16) + h * P::HALF;
-        const uint32_t stage_out = tc::smem_u32(smem + P::OFF_OUT + (warp - 4) * 2048);
-        O *out = static_cast<O *>(p.out);
-        int i = 0;
-        for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
-            const Tile x = tile_of<P, W>(p, seg, first, t);
-            f32x2 acc[P::HALF / 2];
-#pragma unroll
-            for (int j = 0; j < P::HALF / 2; ++j) acc[j] = 0;
+            __syncwarp();
+        } else if (warp != 2) {
+            // Two warps take the even and the odd blocks, each with its accumulator: while one's
+            // MMAs run the other goes through its waits, 100 cycles and more each beside the
+            // tensor cores' own traffic (one warp alone: 640 of 1420 cycles a block).  Each
+            // collects the epilogue's word that its accumulator is read; the first CTA's issue
+            // the MMAs, the second's pass that word on.  After a fault they only keep the
+            // barriers going.
+            const int b = warp >> 1;
+            static_assert(P::STAGES % 2 == 0, "a warp's blocks are every second stage");
+            const uint64_t da0 = tc::desc_kmajor_sw128(tc::smem_u32(smem));
+            const uint64_t db0 = tc::desc_kmajor_sw128(tc::smem_u32(smem) + P::A_BYTES);
+            const uint32_t d0 = tmem + b * P::BN;
+            int st = b, done = 0;       // stage; blocks of this warp so far
+            uint32_t ph = 0, aph = 1;   // phases of the stage's and the accumulator's barrier
             bool ok = true;
-            for (int kb = 0; kb < x.nkb; ++kb, ++i) {
-                const int s = i % P::SC, b = i & 1;
-                if (*abort_flag ||
-                    !tc::mbar_wait(&sc_full[s], (i / P::SC) & 1, p.fault, tc::kFaultTimeoutFull) ||
-                    !tc::mbar_wait(&acc_full[b], (i >> 1) & 1, p.fault, tc::kFaultTimeoutAcc)) {
-                    *abort_flag = 1;
+            auto collect = [&]() {  // this warp's oldest block: accumulator and scales are read
+                tc::named_bar_sync(bar_read(b), 32 * (P::EPI_WARPS + 1));
+                if (lane == 0) {
+                    if (rank) {
+                        tc::tc_fence_after();
+                        tc::tc_fence_before();
+                        arrive_first(&acc_empty[b]);
+                    }
+                    collected[b] = collected[b] + 1;
+                }
+            };
+            int par = b;  // the first block of the next tile that is this warp's
+            for (int t = t0; t < ntiles; t += tstep) {
+                const int nkb = blocks_of<W>(p, seg, t);
+                int kb = par;
+                for (; kb < nkb; kb += 2, ++done) {
+                    if (rank) {
+                        collect();
+                        continue;
+                    }
+                    if (done) collect();
+                    if (lane == 0 && ok) {
+                        ok = tc::mbar_wait(&full[st], ph, p.fault, tc::kFaultTimeoutFull) &&
+                             (CG == 1 ||
+                              tc::mbar_wait(&acc_empty[b], aph, p.fault, tc::kFaultTimeoutAcc));
+                        if (!ok) *abort_flag = 1;
+                    }
+                    if (lane == 0 && ok) {
+                        tc::tc_fence_after();
+                        const uint64_t da = da0 + st * (P::STAGE >> 4), db = db0 + st * (P::STAGE >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < BK / 32; ++kk)
+                            mma_f8<CG>(d0, da + 2 * kk, db + 2 * kk, p.idesc, kk > 0);
+                        commit<CG>(&empty[st]);
+                        commit<CG>(&acc_full[b]);
+                    }
+                    aph ^= 1;
+                    st += 2;
+                    if (st >= P::STAGES) {
+                        st -= P::STAGES;
+                        ph ^= 1;
+                    }
+                    __syncwarp();
+                }
+                par = kb - nkb;
+            }
+            if (rank == 0 && done) collect();
+        } else {
+            // Brings each block's scales, AHEAD blocks before they are read, and waits for the
+            // products and the scales for the epilogue: one warp at the barriers in shared
+            // memory, which the tensor cores keep busy, not sixteen.
+            Cursor<P, W> c(p, seg, first, t0, tstep, ntiles, rank, lane);
+            const uint32_t ring = tc::smem_u32(scales);
+            uint32_t slot = 0;
+            int ahead = 0;  // blocks whose scales are brought and not yet passed on
+            int i = 0;
+            bool ok = true;
+            for (;;) {
+                while (ahead < P::AHEAD && c.left) {
+                    c.load(p, ring + slot);
+                    slot = slot == (P::SC - 1) * P::SC_FLOATS * 4 ? 0 : slot + P::SC_FLOATS * 4;
+                    ++ahead;
+                    c.next(p, seg, first, rank, lane);
+                }
+                if (ahead == 0) break;
+                if (ahead == P::AHEAD)
+                    asm volatile("cp.async.wait_group %0;" ::"n"(P::AHEAD - 1) : "memory");
+                else
+                    tc::cp_async_wait_all();
+                const int b = i & 1;
+                if (ok && !tc::mbar_wait(&acc_full[b], (i >> 1) & 1, p.fault, tc::kFaultTimeoutAcc)) {
                     ok = false;
-                    break;
+                    *abort_flag = 1;
+                }
+                // after a fault the epilogue runs on, block by block
+                for (const long long c0 = clock64();
+                     !ok && collected[b] < (i >> 1) && clock64() - c0 < tc::kWaitCycles;) {
                 }
                 tc::tc_fence_after();
-                const uint32_t sc = tc::smem_u32(scales + s * P::SC_FLOATS);
-                float r = lds32f(sc + (q * 32 + lane) * 4);
-                if (!W) r *= lds32f(sc + (BM + h * P::HALF / 128) * 4);
-                const f32x2 r2 = f2_make(r, r);
-#pragma unroll
-                for (int c = 0; c < P::HALF / 32; ++c) {
-                    f32x2 d[16];
-                    tmem_ld32_wait(trow + b * P::BN + c * 32, d);
-                    if (W) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint4 v = lds128(sc + (BM + h * P::HALF + c * 32 + j * 4) * 4);
-                            const f32x2 s0 = f2_make(__uint_as_float(v.x), __uint_as_float(v.y));
-                            const f32x2 s1 = f2_make(__uint_as_float(v.z), __uint_as_float(v.w));
-                            acc[c * 16 + 2 * j] =
-                                f2_fma(d[2 * j], f2_mul(r2, s0), acc[c * 16 + 2 * j]);
-                            acc[c * 16 + 2 * j + 1] =
-                                f2_fma(d[2 * j + 1], f2_mul(r2, s1), acc[c * 16 + 2 * j + 1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            acc[c * 16 + j] = f2_fma(d[j], r2, acc[c * 16 + j]);
-                    }
-                }
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    tc::mbar_arrive(&acc_empty[b]);
-                    tc::mbar_arrive(&sc_empty[s]);
+#pragma unroll
+                for (int h = 0; h < P::GROUPS; ++h) bar_arrive(bar_ready(h, b), 160);
+                ++i;
+                --ahead;
+            }
+        }
+    } else {
+        if constexpr (CG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        const int q = warp & 3, h = (warp - 4) >> 2;
+        const int g = lane >> 2, tig = lane & 3;
+        const uint32_t trow = tmem + (uint32_t(q * 32) << 16) + h * P::COLS;
+        const uint32_t box = tc::smem_u32(smem + P::OFF_OUT + (warp - 4) * P::BOX);
+        O *out = static_cast<O *>(p.out);
+        const uint32_t sc0 = tc::smem_u32(scales);
+        uint32_t slot = 0;
+        int b = 0;
+        for (int t = t0; t < ntiles; t += tstep) {
+            const Tile x = tile_of<P, W>(p, seg, first, t, rank);
+            // rows: acc[c], row q*32 + lane, column c;  weights: acc[16 n + v], fragment v
+            // (tmem_ld16x32) of rows 16 (n % 2), columns 32 (n / 2)
+            float acc[P::COLS];
+#pragma unroll
+            for (int j = 0; j < P::COLS; ++j) acc[j] = 0.f;
+            for (int kb = 0; kb < x.nkb; ++kb, b ^= 1) {
+                tc::named_bar_sync(bar_ready(h, b), 160);
+                tc::tc_fence_after();
+                const uint32_t sc = sc0 + slot;
+                slot = slot == (P::SC - 1) * P::SC_FLOATS * 4 ? 0 : slot + P::SC_FLOATS * 4;
+                float r[4];
+                float d[16];
+                if constexpr (!W) tmem_ld16(trow + b * P::BN, d);
+                if (W) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) r[j] = lds32f(sc + (q * 32 + 8 * j + g) * 4);
+                } else {
+                    r[0] = lds32f(sc + (q * 32 + lane) * 4) *
+                           lds32f(sc + (BM + h * P::COLS / 128) * 4);
+                }
+                const uint32_t d0 = trow + b * P::BN;
+                // the accumulator goes back as soon as its last columns are in registers
+                auto release = [&]() {
+                    tc::tc_fence_before();
+                    bar_arrive(bar_read(b), 32 * (P::EPI_WARPS + 1));
+                };
+                if constexpr (W) {
+                    constexpr int NL = P::COLS / 16;  // loads of 16 lanes x 32 columns
+                    float c[8];
+#pragma unroll
+                    for (int n = 0; n < NL; ++n) {
+                        if (n % 2 == 0) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint2 u = lds64(
+                                    sc + (BM + h * P::COLS + (n / 2) * 32 + 8 * j + 2 * tig) * 4);
+                                c[2 * j] = __uint_as_float(u.x);
+                                c[2 * j + 1] = __uint_as_float(u.y);
+                            }
+                        }
+                        float &r0 = r[2 * (n & 1)], &r1 = r[2 * (n & 1) + 1];
+                        tmem_ld16x32(d0 + (n / 2) * 32 + (uint32_t(n & 1) << 20), d);
+                        tmem_wait(r0, r1);
+                        if (n + 1 == NL) release();
+                        float *ac = acc + 16 * n;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            ac[4 * j] = fmaf(d[4 * j], c[2 * j] * r0, ac[4 * j]);
+                            ac[4 * j + 1] = fmaf(d[4 * j + 1], c[2 * j + 1] * r0, ac[4 * j + 1]);
+                            ac[4 * j + 2] = fmaf(d[4 * j + 2], c[2 * j] * r1, ac[4 * j + 2]);
+                            ac[4 * j + 3] = fmaf(d[4 * j + 3], c[2 * j + 1] * r1, ac[4 * j + 3]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < P::COLS / 16; ++c) {
+                        if (c) tmem_ld16(d0 + c * 16, d);
+                        tmem_wait(r[0]);
+                        if (c + 1 == P::COLS / 16) release();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fmaf(d[j], r[0], acc[c * 16 + j]);
+                    }
                 }
             }
-            if (!ok) break;
-            // rounded once, through shared memory in pieces of 64 bytes a row:
-            // whole sectors leave (a row a lane would write 16 bytes of each)
-            constexpr int VN = 16 / int(sizeof(O)), CH = 4 * VN;
-            const int64_t row_base = W ? int64_t(x.e) * p.out_rows : 0;
+            if (*abort_flag) continue;
+            // rounded once, 128 bytes of each of the warp's 32 rows at a time
+            constexpr int VN = 16 / int(sizeof(O)), CH = 8 * VN;
+            const int wrow = x.row0 + q * 32, col0 = x.n0 + h * P::COLS;
+            const bool whole = W ? wrow < x.row_end : wrow + 32 <= x.row_end;
+            if (wrow >= x.row_end) continue;
 #pragma unroll
-            for (int c = 0; c < P::HALF / CH; ++c) {
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    float f[VN];
-#pragma unroll
-                    for (int j = 0; j < VN / 2; ++j)
-                        f2_split(acc[(c * CH + v * VN) / 2 + j], f[2 * j], f[2 * j + 1]);
-                    Vec<O, VN> o;
-                    narrow<O, VN>(f, o);
-                    const uint32_t at = stage_out + lane * 64 + ((v ^ ((lane >> 1) & 3)) * 16);
-                    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(o.w[0]),
-                                 "r"(o.w[1]), "r"(o.w[2]), "r"(o.w[3])
-                                 : "memory");
-                }
+            for (int c = 0; c < P::COLS / CH; ++c) {
+                if (col0 + c * CH >= p.N) break;
+                if (lane == 0) tc::bulk_wait_read_all();
                 __syncwarp();
+                if constexpr (!W) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = j * 8 + (lane >> 2), v = lane & 3;
-                    const uint4 u = lds128(stage_out + r * 64 + ((v ^ ((r >> 1) & 3)) * 16));
-                    const int row = x.row0 + q * 32 + r;
-                    const int64_t col = x.n0 + h * P::HALF + c * CH + v * VN;
-                    if (row < x.row_end && col < p.N)
-                        st_stream(out + (row_base + row) * p.N + col, u);
+                    for (int v = 0; v < 8; ++v) {
+                        float f[VN];
+#pragma unroll
+                        for (int j = 0; j < VN; ++j) f[j] = acc[c * CH + v * VN + j];
+                        Vec<O, VN> o;
+                        narrow<O, VN>(f, o);
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                         box + lane * 128 + ((v ^ (lane & 7)) * 16)),
+                                     "r"(o.w[0]), "r"(o.w[1]), "r"(o.w[2]), "r"(o.w[3])
+                                     : "memory");
+                    }
+                } else {
+#pragma unroll
+                    for (int hi = 0; hi < 2; ++hi)
+#pragma unroll
+                        for (int jj = 0; jj < CH / 8; ++jj)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int cc = c * CH + 8 * jj;  // columns cc + 2 tig, + 1
+                                const float *v = acc + 16 * (2 * (cc / 32) + hi) + 4 * (cc % 32 / 8) + 2 * k;
+                                const int row = 16 * hi + 8 * k + g;
+                                const int byte = (8 * jj + 2 * tig) * int(sizeof(O));
+                                const uint32_t to = box + row * 128 + (((byte >> 4) ^ g) << 4) + (byte & 15);
+                                if constexpr (sizeof(O) == 4)
+                                    asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(to), "f"(v[0]),
+                                                 "f"(v[1])
+                                                 : "memory");
+                                else
+                                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(to),
+                                                 "r"(round2(v[0], v[1], static_cast<const O *>(nullptr)))
+                                                 : "memory");
+                            }
                 }
-                __syncwarp();
+                if (whole) {
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (W)
+                            store_3d(&tmo, box, col0 + c * CH, wrow, x.e);
+                        else
+                            store_2d(&tmo, box, col0 + c * CH, wrow);
+                        tc::bulk_commit_group();
+                    }
+                } else {
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int r = j * 4 + (lane >> 3), v = lane & 7;
+                        const uint4 u = lds128(box + r * 128 + ((v ^ (r & 7)) * 16));
+                        const int64_t col = col0 + c * CH + v * VN;
+                        if (wrow + r < x.row_end && col < p.N)
+                            st_stream(out + int64_t(wrow + r) * p.N + col, u);
+                    }
+                }
             }
         }
         // the rows of no segment
         if (!W && !*abort_flag) {
-            const int64_t n0 = int64_t(row_first) * p.N, n1 = int64_t(row_last) * p.N;
+            const int64_t n0 = int64_t(seg[0]) * p.N, n1 = int64_t(seg[p.G]) * p.N;
             constexpr int VN = 16 / int(sizeof(O));
             const int64_t all = (int64_t(p.R) * p.N - n1 + n0) / VN;
             const int64_t step = int64_t(gridDim.x) * (32 * P::EPI_WARPS);
@@ -463,39 +807,83 @@ __global__ void __launch_bounds__(P::THREADS, 1)
                 st_stream(out + el, make_uint4(0, 0, 0, 0));
             }
         }
+        if (lane == 0) tc::bulk_wait_all();
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 1) tc::tmem_dealloc(tmem, P::TMEM_COLS);
+    if constexpr (CG == 2) cluster_sync();  // nothing of the other CTA's reaches in here any more
+    if (warp == 1) tmem_dealloc<CG>(tmem, P::TMEM_COLS);
+}
+
+// CTAs (a multiple of CG) that run at one time, one an SM.
+template <int CG, class K>
+cudaError_t resident(K *kernel, int threads, int smem, int64_t *ctas)
+{
+    *ctas = num_sms();
+    if (CG == 1) return cudaSuccess;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(*ctas / CG * CG));
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {CG, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    *ctas = int64_t(n > 0 ? n : 1) * CG;
+    return e;
 }
 
 template <class P, bool W, class O>
-cudaError_t run(const CUtensorMap &ta, const CUtensorMap &tb, const GemmP &p, int64_t tiles,
-                cudaStream_t s)
+cudaError_t run(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &to, const GemmP &p,
+                int64_t tiles, cudaStream_t s)
 {
     auto *kernel = k_fp8_gemm<P, W, O>;
     cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kernel), P::SMEM);
     if (e != cudaSuccess) return e;
-    const int64_t sms = num_sms();
+    static std::atomic<int64_t> known[64];  // by device
+    int dev = 0;
+    e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int64_t ctas = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (ctas == 0) {
+        e = resident<P::CG>(kernel, P::THREADS, P::SMEM, &ctas);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) known[dev].store(ctas, std::memory_order_relaxed);
+    }
     MHC_PROF(W ? "k_fp8_wgrad" : "k_fp8_gemm", s);
-    return launch_k(kernel, dim3(unsigned(std::min(sms, std::max<int64_t>(tiles, 1)))),
-                    dim3(P::THREADS), P::SMEM, s, ta, tb, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min(ctas, std::max<int64_t>(tiles, 1) * P::CG)));
+    cfg.blockDim = dim3(P::THREADS);
+    cfg.dynamicSmemBytes = P::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {P::CG, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = P::CG == 1 ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, kernel, ta, tb, to, p);
 }
 
 template <class P, bool W>
-cudaError_t by_type(const CUtensorMap &ta, const CUtensorMap &tb, const GemmP &p, int64_t tiles,
-                    int out_dtype, cudaStream_t s)
+cudaError_t by_type(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &to,
+                    const GemmP &p, int64_t tiles, int out_dtype, cudaStream_t s)
 {
-    if (out_dtype == 0) return run<P, W, bf16>(ta, tb, p, tiles, s);
-    if (out_dtype == 1) return run<P, W, fp16>(ta, tb, p, tiles, s);
-    return run<P, W, float>(ta, tb, p, tiles, s);
+    if (out_dtype == 0) return run<P, W, bf16>(ta, tb, to, p, tiles, s);
+    if (out_dtype == 1) return run<P, W, fp16>(ta, tb, to, p, tiles, s);
+    return run<P, W, float>(ta, tb, to, p, tiles, s);
 }
 
-}  // namespace
+typedef GemmCfg<1, 128> One;
+typedef GemmCfg<2, 256> Pair;
 
-cudaError_t launch_fp8_gemm(const Fp8GemmArgs &a, int out_dtype, cudaStream_t s)
+template <class P>
+cudaError_t gemm_rows(const Fp8GemmArgs &a, int out_dtype, cudaStream_t s)
 {
-    typedef GemmCfg<256> P;
     GemmP p = {};
     p.sa = a.sa;
     p.sb = a.sb;
@@ -506,24 +894,27 @@ cudaError_t launch_fp8_gemm(const Fp8GemmArgs &a, int out_dtype, cudaStream_t s)
     p.R = int(a.R);
     p.nkb = int(fp8_blocks(a.K));
     p.nt = int((a.N + P::BN - 1) / P::BN);
-    p.idesc = idesc_f8_f32(a.fa, a.fb, BM, P::BN);
+    p.idesc = idesc_f8_f32(a.fa, a.fb, P::CG * BM, P::BN);
     p.out = a.out;
     p.fault = a.fault;
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, to;
+    const uint64_t es = out_dtype == 2 ? 4 : 2;
     const uint64_t da[2] = {uint64_t(a.K), uint64_t(a.R)}, ra[1] = {uint64_t(a.K)};
     const uint64_t db[3] = {uint64_t(a.K), uint64_t(a.N), uint64_t(a.G)};
     const uint64_t rb[2] = {uint64_t(a.K), uint64_t(a.K) * uint64_t(a.N)};
-    const uint32_t ba[2] = {BK, BM}, bb[3] = {BK, P::BN, 1};
-    if (!tmap_u8(&ta, a.a, 2, da, ra, ba) || !tmap_u8(&tb, a.b, 3, db, rb, bb))
+    const uint64_t dn[2] = {uint64_t(a.N), uint64_t(a.R)}, rn[1] = {uint64_t(a.N) * es};
+    const uint32_t ba[2] = {BK, BM}, bb[3] = {BK, 128, 1}, bo[2] = {uint32_t(128 / es), 32};
+    if (!tmap_u8(&ta, a.a, 2, da, ra, ba) || !tmap_u8(&tb, a.b, 3, db, rb, bb) ||
+        !tmap_out(&to, a.out, out_dtype, 2, dn, rn, bo))
         return cudaErrorInvalidValue;
     // a bound on the tiles: every segment may end inside one
-    const int64_t tiles = (a.R / BM + std::min(a.G, a.R)) * p.nt;
-    return by_type<P, false>(ta, tb, p, tiles, out_dtype, s);
+    const int64_t tiles = (a.R / (P::CG * BM) + std::min(a.G, a.R)) * p.nt;
+    return by_type<P, false>(ta, tb, to, p, tiles, out_dtype, s);
 }
 
-cudaError_t launch_fp8_wgrad(const Fp8WgradArgs &a, int out_dtype, cudaStream_t s)
+template <class P>
+cudaError_t gemm_weights(const Fp8WgradArgs &a, int out_dtype, cudaStream_t s)
 {
-    typedef GemmCfg<256> P;
     GemmP p = {};
     p.sa = a.sa;
     p.sb = a.sb;
@@ -532,18 +923,34 @@ cudaError_t launch_fp8_wgrad(const Fp8WgradArgs &a, int out_dtype, cudaStream_t 
     p.N = a.N;
     p.G = int(a.G);
     p.R = int(a.R);
-    p.mt = int((a.M + BM - 1) / BM);
+    p.mt = int((a.M + P::CG * BM - 1) / (P::CG * BM));
     p.nt = int((a.N + P::BN - 1) / P::BN);
-    p.idesc = idesc_f8_f32(a.fa, a.fb, BM, P::BN);
+    p.idesc = idesc_f8_f32(a.fa, a.fb, P::CG * BM, P::BN);
     p.out = a.out;
     p.fault = a.fault;
-    CUtensorMap ta, tb;
+    CUtensorMap ta, tb, to;
+    const uint64_t es = out_dtype == 2 ? 4 : 2;
     const uint64_t da[2] = {uint64_t(a.R), uint64_t(a.M)}, db[2] = {uint64_t(a.R), uint64_t(a.N)};
     const uint64_t r[1] = {uint64_t(a.R)};
-    const uint32_t ba[2] = {BK, BM}, bb[2] = {BK, P::BN};
-    if (!tmap_u8(&ta, a.a, 2, da, r, ba) || !tmap_u8(&tb, a.b, 2, db, r, bb))
+    const uint64_t dn[3] = {uint64_t(a.N), uint64_t(a.M), uint64_t(a.G)};
+    const uint64_t rn[2] = {uint64_t(a.N) * es, uint64_t(a.N) * uint64_t(a.M) * es};
+    const uint32_t ba[2] = {BK, BM}, bb[2] = {BK, 128}, bo[3] = {uint32_t(128 / es), 32, 1};
+    if (!tmap_u8(&ta, a.a, 2, da, r, ba) || !tmap_u8(&tb, a.b, 2, db, r, bb) ||
+        !tmap_out(&to, a.out, out_dtype, 3, dn, rn, bo))
         return cudaErrorInvalidValue;
-    return by_type<P, true>(ta, tb, p, a.G * p.mt * p.nt, out_dtype, s);
+    return by_type<P, true>(ta, tb, to, p, a.G * p.mt * p.nt, out_dtype, s);
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_gemm(const Fp8GemmArgs &a, int out_dtype, cudaStream_t s)
+{
+    return a.R >= 160 * a.G ? gemm_rows<Pair>(a, out_dtype, s) : gemm_rows<One>(a, out_dtype, s);
+}
+
+cudaError_t launch_fp8_wgrad(const Fp8WgradArgs &a, int out_dtype, cudaStream_t s)
+{
+    return a.M > BM ? gemm_weights<Pair>(a, out_dtype, s) : gemm_weights<One>(a, out_dtype, s);
 }
 
 }  // namespace mhc

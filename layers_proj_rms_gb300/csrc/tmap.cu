@@ -53,6 +53,15 @@ bool tmap_u8(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
                        CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+bool tmap_out(CUtensorMap *m, const void *base, int dtype, int rank, const uint64_t *dims,
+              const uint64_t *strides_bytes, const uint32_t *box)
+{
+    const CUtensorMapDataType t = dtype == 0   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                  : dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    return tmap_encode(m, t, base, rank, dims, strides_bytes, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 bool tmap_f32_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                  uint32_t box_cols, CUtensorMapSwizzle sw)
 {

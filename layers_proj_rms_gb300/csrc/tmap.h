@@ -27,6 +27,11 @@ inline bool tmap_bf16_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64
 bool tmap_u8(CUtensorMap *m, const void *base, int rank, const uint64_t *dims,
              const uint64_t *strides_bytes, const uint32_t *box);
 
+// A tensor of activations (0 bf16, 1 fp16, 2 fp32) that is stored in boxes of 128-byte rows, in the
+// 128-byte swizzle.
+bool tmap_out(CUtensorMap *m, const void *base, int dtype, int rank, const uint64_t *dims,
+              const uint64_t *strides_bytes, const uint32_t *box);
+
 // A row-major [rows][cols] fp32 matrix, box [box_rows][box_cols].
 bool tmap_f32_2d(CUtensorMap *m, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows,
                  uint32_t box_cols, CUtensorMapSwizzle sw);
