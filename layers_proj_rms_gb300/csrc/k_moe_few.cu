@@ -1,7 +1,8 @@
-// The whole experts' layer for a few tokens, in two launches:
+// The whole experts' layer for a few tokens, in two launches and a short one:
 //
 //   up:    h[t,j] = silu(W1g[e] x[t]) * (W1u[e] x[t]),  e = ids[t][j]
-//   down:  f[t] = sum_j w[t][j] W2[e] h[t,j]
+//   down:  y[t,j] = W2[e] h[t,j]
+//   sum:   f[t] = sum_j w[t][j] y[t,j]
 //
 // Few tokens read far more weights than anything else, so the weights go by once
 // and straight into registers: a warp's piece is 128 bytes of 32 weight rows,
@@ -13,8 +14,8 @@
 //
 // Work: (segment, tile) in order of the experts, a segment up to 8 or 16 slots
 // of one expert, a tile 32 weight rows (16 of gate and the same 16 of up); a
-// block, one an SM, takes a contiguous share of it.  Up to 16 warps split a
-// tile's k in pieces and join through shared memory in a fixed order.  The next
+// block, one an SM, takes a contiguous share of it.  One to 16 warps split a
+// tile's k in pieces and join through shared memory in a fixed order (split_of).  The next
 // piece is always in flight: 16 warps x 4 KB an SM.
 //
 // 16-bit weights: x as it is; h as two terms of the type (its rounding and the
@@ -22,8 +23,10 @@
 // quantised by blocks of 128, as mhc_fp8_quant does, when a segment's rows are
 // brought to shared memory; each block's product is scaled into fp32 sums.
 //
-// down writes each slot's row and the last block at a tile of columns adds up
-// the tokens' slots in their order: nothing depends on which block that is.
+// A slot's row of y is written once and a token's slots are added up in their
+// order, so nothing depends on which block did what.  (The last block at a tile of
+// columns adding them up, found by counts, took longer: the counts' round trips at
+// every tile, and nearly all of the sums in the one block with the last segment.)
 #include <algorithm>
 
 #include "elem.cuh"
@@ -54,8 +57,6 @@ struct FewP {
     int wk;               // warps that split a tile's k
     void *h;              // [T*k, F] fp32, or two terms of the type
     float *y;             // [T*k, C]
-    int *count;           // [tiles of C]
-    void *f;
     int64_t F, C;
     int *fault;
 };
@@ -114,16 +115,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
     uint16_t *slots = reinterpret_cast<uint16_t *>(smem);
     int *first = reinterpret_cast<int *>(smem + kMaxSlots * 2);
     int *fseg = first + 1028;
-    int *flags = fseg + 1028;  // [16]
-    float *red = reinterpret_cast<float *>(flags + 16);  // [2][warps][TOK][kPitch]
+    float *red = reinterpret_cast<float *>(fseg + 1028);  // [2][warps][TOK][kPitch]
     uint8_t *xs = reinterpret_cast<uint8_t *>(red + 2 * kWarps * TOK * kPitch);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, tig = lane & 3;
     const int n = p.T * p.k, E = p.E;
 
-    // What the ids say was there before the first launch began; only h, y and
-    // the counts are its work.
+    // What the ids say was there before the first launch began; only h is its work.
     if (!DOWN) pdl_wait();
     int *ids = reinterpret_cast<int *>(red);  // not in use yet
     for (int i = tid; i < n; i += kThreads) {
@@ -134,8 +133,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
         }
         ids[i] = e;
     }
-    if (!DOWN && blockIdx.x == 0)
-        for (int i = tid; i < int((p.C + kRows - 1) / kRows); i += kThreads) p.count[i] = 0;
     __syncthreads();
     for (int e = tid; e < E; e += kThreads) {
         int c = 0;
@@ -193,16 +190,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
     float *sx = reinterpret_cast<float *>(xs + (EIGHT ? TOK * xpitch : 0));  // [nkb][TOK]
     const uint8_t *wt = static_cast<const uint8_t *>(p.wt);
 
-    if (DOWN && nseg == 0) {  // every slot is dropped
-        pdl_wait();
-        X *f = static_cast<X *>(p.f);
-        Vec<X, 8> z;
-        zero_vec<X, 8>(z);
-        for (int64_t i = int64_t(blockIdx.x) * kThreads + tid; i < p.T * p.C / 8;
-             i += int64_t(gridDim.x) * kThreads)
-            st_vec<X, 8>(f + i * 8, z);
-        return;
-    }
     const int64_t total = int64_t(nseg) * p.ntiles;
     const int64_t t_begin = total * blockIdx.x / gridDim.x;
     const int64_t t_end = total * (blockIdx.x + 1) / gridDim.x;
@@ -410,29 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
                     if (row >= p.C) continue;
                     float y = 0.f;
                     for (int w = 0; w < WK; ++w) y += all[(w * TOK + t) * kPitch + r];
-                    __stcg(p.y + int64_t(slots[s0 + t]) * p.C + row, y);
-                }
-                // the last segment at this tile adds up the tokens' slots
-                __threadfence();
-                group_sync();
-                if (gtid == 0) flags[gi] = atomicAdd(p.count + tl, 1) == nseg - 1;
-                group_sync();
-                if (flags[gi]) {
-                    __threadfence();
-                    X *f = static_cast<X *>(p.f);
-                    for (int o = gtid; o < p.T * 32; o += gsize) {
-                        const int64_t col = int64_t(tl) * kRows + (o & 31);
-                        const int t = o >> 5;
-                        if (col >= p.C) continue;
-                        float sum = 0.f;
-                        for (int j = 0; j < p.k; ++j) {
-                            const int slot = t * p.k + j, ex = __ldg(p.ids + slot);
-                            if (ex >= 0 && ex < E)
-                                sum = fmaf(__ldg(p.w + slot), __ldcg(p.y + int64_t(slot) * p.C + col),
-                                           sum);
-                        }
-                        f[int64_t(t) * p.C + col] = X(sum);
-                    }
+                    p.y[int64_t(slots[s0 + t]) * p.C + row] = y;
                 }
             }
         };
@@ -463,21 +428,64 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
     if (!waited) pdl_wait();
 }
 
+// f[t] = sum over the token's slots, in their order, of w y; 8 columns a thread.
+template <class X>
+__global__ void __launch_bounds__(128) k_moe_few_sum(const float *__restrict__ y,
+                                                     const int32_t *__restrict__ ids,
+                                                     const float *__restrict__ w, int T, int k, int E,
+                                                     int64_t C, X *__restrict__ f)
+{
+    const int64_t i = int64_t(blockIdx.x) * 128 + threadIdx.x, per = C / 8;
+    const int t = int(i / per);
+    const int64_t c = (i - t * per) * 8;
+    pdl_wait();
+    if (t >= T) return;
+    float sum[8] = {};
+    for (int j = 0; j < k; ++j) {
+        const int slot = t * k + j, e = __ldg(ids + slot);
+        if (e < 0 || e >= E) continue;
+        const float *row = y + int64_t(slot) * C + c;
+        const float4 a = *reinterpret_cast<const float4 *>(row), b = *reinterpret_cast<const float4 *>(row + 4);
+        const float m = __ldg(w + slot), v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] = fmaf(m, v[q], sum[q]);
+    }
+    Vec<X, 8> o;
+    narrow<X, 8>(sum, o);
+    st_vec<X, 8>(f + t * C + c, o);
+}
+
 size_t few_smem(int NT, bool eight, int64_t K)
 {
     const int64_t nkb = fp8_blocks(K), tok = 8 * NT;
-    int64_t b = kMaxSlots * 2 + (1028 * 2 + 16) * 4 + 2 * kWarps * tok * kPitch * 4;
+    int64_t b = kMaxSlots * 2 + 1028 * 2 * 4 + 2 * kWarps * tok * kPitch * 4;
     if (eight) b += tok * (nkb * kFp8Block + 64) + nkb * tok * 4;
     return size_t(b);
 }
 constexpr size_t kSmemMax = 232448;
 
-int split_of(int64_t K, int bytes)
+// How many of a block's 16 warps split a tile's k.  More of them finish a tile
+// sooner but join more often, which costs a warp about two pieces' time; fewer
+// leave warps without a tile where a block has few.  So the least of tiles in
+// turn x (pieces of a warp + 2), for as many segments as the slots can make; but
+// four at least, whose pieces are 512 bytes in a row (13 tokens, 4096 x 1408, 60
+// experts, 16 bits: 315 us with one, 269 with two, 226 with four, 219 with eight).
+int split_of(int64_t K, int bytes, int64_t tiles)
 {
     const int64_t np = (K * bytes + kPiece - 1) / kPiece;
-    int w = 1;
-    while (w < kWarps && 2 * w <= np) w *= 2;
-    return w;
+    const double per_block = double(tiles) / num_sms();
+    int best = int(std::min<int64_t>(np, 4));
+    best = best == 3 ? 2 : best;
+    double least = 1e30;
+    for (int w = best; w <= kWarps && w <= np; w *= 2) {
+        const double turns = per_block * w / kWarps;
+        const double cost = (turns < 1 ? 1 : turns) * double((np + w - 1) / w + 2);
+        if (cost < least) {
+            least = cost;
+            best = w;
+        }
+    }
+    return best;
 }
 
 template <class W, class X, int NT, bool DOWN>
@@ -508,7 +516,8 @@ cudaError_t both(FewP &p, const MoeFewArgs &a, cudaStream_t s)
     p.K = a.C;
     p.rows = 2 * a.F;
     p.ntiles = int(a.F / 16);
-    p.wk = split_of(p.K, sizeof(W));
+    const int64_t segments = std::min<int64_t>(a.E, a.T * a.k);
+    p.wk = split_of(p.K, sizeof(W), segments * p.ntiles);
     cudaError_t e = by_columns<W, X, false>(p, s);
     if (e != cudaSuccess) return e;
     p.wt = a.w2;
@@ -516,16 +525,21 @@ cudaError_t both(FewP &p, const MoeFewArgs &a, cudaStream_t s)
     p.K = a.F;
     p.rows = a.C;
     p.ntiles = int((a.C + kRows - 1) / kRows);
-    p.wk = split_of(p.K, sizeof(W));
-    return by_columns<W, X, true>(p, s);
+    p.wk = split_of(p.K, sizeof(W), segments * p.ntiles);
+    e = by_columns<W, X, true>(p, s);
+    if (e != cudaSuccess) return e;
+    const int64_t n = a.T * (a.C / 8);
+    MHC_PROF("k_moe_few_sum", s);
+    return launch_k(k_moe_few_sum<X>, dim3(unsigned((n + 127) / 128)), dim3(128), 0, s,
+                    static_cast<const float *>(p.y), p.ids, p.w, p.T, p.k, p.E, p.C,
+                    static_cast<X *>(a.f));
 }
 
 }  // namespace
 
 size_t moe_few_ws_bytes(int64_t T, int k, int64_t CF)
 {
-    // h and y, a count for each 32 columns
-    return ws_align(size_t(T) * size_t(k) * size_t(CF) * 4) + ws_align(size_t(CF / kRows + 2) * 4) + 256;
+    return ws_align(size_t(T) * size_t(k) * size_t(CF) * 4) + 256;  // h and y
 }
 
 cudaError_t launch_moe_few(const MoeFewArgs &a, int dtype, int eight, cudaStream_t s)
@@ -539,13 +553,11 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, int dtype, int eight, cudaStream
     p.E = a.E;
     p.F = a.F;
     p.C = a.C;
-    p.f = a.f;
     p.fault = a.fault;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     const size_t n = size_t(a.T) * size_t(a.k);
     p.h = ws;
     p.y = reinterpret_cast<float *>(ws + n * size_t(a.F) * 4);
-    p.count = reinterpret_cast<int *>(ws + ws_align(n * size_t(a.F + a.C) * 4));
     if (eight) return dtype == 0 ? both<E4m3, bf16>(p, a, s) : both<E4m3, fp16>(p, a, s);
     return dtype == 0 ? both<bf16, bf16>(p, a, s) : both<fp16, fp16>(p, a, s);
 }
