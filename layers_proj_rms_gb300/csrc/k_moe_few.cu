@@ -9,11 +9,13 @@
 // 16 bytes a lane and load, in the order of a tensor-core operand's words (the
 // product does not care about the order of k as long as both operands have the
 // same), the tokens are the other operand's 8 columns.  mma.sync, not tcgen05:
-// there are 8 or 16 columns, the tensor cores are far from busy, and operands
-// that stay in registers need no trip through shared memory.
+// there are 8 columns, the tensor cores are far from busy, and operands that stay
+// in registers need no trip through shared memory.
 //
-// Work: (segment, tile) in order of the experts, a segment up to 8 or 16 slots
-// of one expert, a tile 32 weight rows (16 of gate and the same 16 of up); a
+// Work: (segment, tile) in order of the experts, a segment up to 8 slots of one
+// expert (16 at a time held twice the sums and took longer wherever it was tried,
+// 329 us for 166 with 16 slots an expert: the second 8 find the weights in L2),
+// a tile 32 weight rows (16 of gate and the same 16 of up); a
 // block, one an SM, takes a contiguous share of it.  One to 16 warps split a
 // tile's k in pieces and join through shared memory in a fixed order (split_of).  The next
 // piece is always in flight: 16 warps x 4 KB an SM.
@@ -28,6 +30,7 @@
 // columns adding them up, found by counts, took longer: the counts' round trips at
 // every tile, and nearly all of the sums in the one block with the last segment.)
 #include <algorithm>
+#include <type_traits>
 
 #include "elem.cuh"
 #include "fp8.cuh"
@@ -40,6 +43,7 @@ namespace {
 
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kRows = 32;                 // weight rows of a tile
+constexpr int TOK = 8;                    // slots of a segment: the tensor cores' columns
 constexpr int kPitch = 36;                // floats of a token's partial sums: no bank conflicts
 constexpr int kMaxSlots = kMoeFewTokens * 32;
 constexpr int kPiece = 128;               // bytes of k a warp takes at once
@@ -63,38 +67,71 @@ struct FewP {
 
 struct E4m3 { uint8_t v; };
 
-template <class W>
+// d = a b + c, c = d or zeros; 16-bit operands of type W
+#define MHC_MMA(type)                                                                               \
+    if (FIRST)                                                                                      \
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." type ".f32 {%0,%1,%2,%3}, "           \
+                     "{%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"                                   \
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                               \
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));             \
+    else                                                                                            \
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." type ".f32 {%0,%1,%2,%3}, "           \
+                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"                                       \
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                               \
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1))
+template <class W, bool FIRST>
 __device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                     uint32_t a3, uint32_t b0, uint32_t b1);
-template <>
-__device__ __forceinline__ void mma8<bf16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                           uint32_t a3, uint32_t b0, uint32_t b1)
+                                     uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-                 "{%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    if constexpr (std::is_same<W, bf16>::value) {
+        MHC_MMA("bf16.bf16");
+    } else {
+        MHC_MMA("f16.f16");
+    }
 }
-template <>
-__device__ __forceinline__ void mma8<fp16>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                           uint32_t a3, uint32_t b0, uint32_t b1)
+#undef MHC_MMA
+
+// Four e4m3 values as two pairs of fp16, which hold them exactly.  Volatile: kept
+// for a second use, the conversions of a piece would take 64 registers.
+__device__ __forceinline__ uint2 widen_e4m3(uint32_t w)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-                 "{%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    uint2 v;
+    asm volatile("{\n"
+        ".reg .b16 lo, hi;\n"
+        "mov.b32 {lo, hi}, %2;\n"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n"
+        "}\n"
+        : "=r"(v.x), "=r"(v.y)
+        : "r"(w));
+    return v;
 }
-template <>
-__device__ __forceinline__ void mma8<E4m3>(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                           uint32_t a3, uint32_t b0, uint32_t b1)
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i)
 {
-    asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-                 "{%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
+
+// 16 bytes that are read once, or zeros: a predicated load, which nothing waits for
+// before its values are used (a choice of values would).
+__device__ __forceinline__ uint4 ld_or_zero(const void *p, bool in)
+{
+    uint4 v;
+    asm volatile(
+        "{\n"
+        ".reg .pred q;\n"
+        "setp.ne.b32 q, %5, 0;\n"
+        "mov.b32 %0, 0;\n"
+        "mov.b32 %1, 0;\n"
+        "mov.b32 %2, 0;\n"
+        "mov.b32 %3, 0;\n"
+        "@q ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+        "}\n"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"(int(in)));
+    return v;
+}
 
 // A warp's piece in flight: for each of two 64-byte steps the 16 bytes of rows
 // g, g + 8, g + 16, g + 24 (g = lane / 4), and the scales of the two row groups.
@@ -105,11 +142,10 @@ struct Piece {
 };
 
 // W: bf16, fp16 or E4m3; X: the activations.
-template <class W, class X, int NT, bool DOWN>
+template <class W, class X, bool DOWN>
 __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
 {
     constexpr bool EIGHT = sizeof(W) == 1;
-    constexpr int TOK = 8 * NT;
     extern __shared__ __align__(16) uint8_t smem[];
     // slots in order of their experts, the experts' first slots and first segments
     uint16_t *slots = reinterpret_cast<uint16_t *>(smem);
@@ -122,8 +158,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
     const int g = lane >> 2, tig = lane & 3;
     const int n = p.T * p.k, E = p.E;
 
-    // What the ids say was there before the first launch began; only h is its work.
+    // The next launch's blocks may come as this one's leave (each fills an SM).  down
+    // begins with ids and weights: all of up's blocks are past their wait then, so what
+    // came before up is done; only h is its work.
     if (!DOWN) pdl_wait();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int *ids = reinterpret_cast<int *>(red);  // not in use yet
     for (int i = tid; i < n; i += kThreads) {
         int e = __ldg(p.ids + i);
@@ -215,28 +254,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
         auto row_of = [&](int tile, int m) {  // first weight row of row group m
             return DOWN ? int64_t(tile) * kRows + m * 16 : m * p.F + int64_t(tile) * 16;
         };
-        auto load = [&](Piece<EIGHT> &b, int tile, int piece) {
-            const int64_t off = int64_t(piece) * kPiece + tig * 16;
+        // this warp's pieces: wk, wk + WK, ... of tiles gi, gi + NG, ...; where the next one
+        // stands is stepped, as an instruction costs a warp beside 15 others five cycles
+        const int tile0 = int(t0 - int64_t(seg) * p.ntiles), tile1 = int(t1 - int64_t(seg) * p.ntiles);
+        int ltile = tile0 + gi, lpiece = wk;
+        const uint8_t *la[2];  // row g of the row groups, this lane's bytes of the piece
+        const float *ls[2];    // the row groups' scales of the piece
+        const int64_t row8 = 8 * Kb;
+        auto seek = [&]() {  // to the first piece of ltile
+            lpiece = wk;
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                int64_t r = row_of(tile, m);
+                int64_t r = row_of(ltile, m);
                 if (DOWN) r = min(r, p.rows - 16);  // a last tile of 16 rows
-                const uint8_t *a = we + (r + g) * Kb + off;
-#pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    const bool in = off + st * 64 < Kb;
-                    b.a[st][2 * m] = in ? ld_stream(a + st * 64) : zero4();
-                    b.a[st][2 * m + 1] = in ? ld_stream(a + 8 * Kb + st * 64) : zero4();
-                }
-                if constexpr (EIGHT)
-                    b.s[m] = __ldg(p.s + (int64_t(e) * nkb + piece) * nrb + r / kFp8Block);
+                la[m] = we + (r + g) * Kb + wk * kPiece + tig * 16;
+                if constexpr (EIGHT) ls[m] = p.s + (int64_t(e) * nkb + wk) * nrb + r / kFp8Block;
             }
         };
-        // this warp's pieces: wk, wk + WK, ... of tiles gi, gi + NG, ...
-        const int tile0 = int(t0 - int64_t(seg) * p.ntiles), tile1 = int(t1 - int64_t(seg) * p.ntiles);
+        auto load = [&](Piece<EIGHT> &b) {  // the next piece
+            if ((lpiece + 1) * kPiece <= Kb) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        b.a[st][2 * m] = ld_stream(la[m] + st * 64);
+                        b.a[st][2 * m + 1] = ld_stream(la[m] + row8 + st * 64);
+                    }
+            } else {
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        const bool in = lpiece * kPiece + tig * 16 + st * 64 < Kb;
+                        b.a[st][2 * m] = ld_or_zero(la[m] + st * 64, in);
+                        b.a[st][2 * m + 1] = ld_or_zero(la[m] + row8 + st * 64, in);
+                    }
+            }
+            if constexpr (EIGHT) {
+                b.s[0] = __ldg(ls[0]);
+                b.s[1] = __ldg(ls[1]);
+            }
+            lpiece += WK;
+            if (lpiece < np) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    la[m] += WK * kPiece;
+                    if constexpr (EIGHT) ls[m] += WK * nrb;
+                }
+            } else {
+                ltile += NG;
+                seek();
+            }
+        };
         Piece<EIGHT> b0, b1;
-        int tile = tile0 + gi, piece = wk;
-        if (tile < tile1) load(b0, tile, piece);
+        int tile = ltile, piece = wk;
+        seek();
+        if (tile < tile1) load(b0);
         if (!waited) {
             pdl_wait();
             waited = true;
@@ -274,98 +347,87 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
             __syncthreads();
         }
         // columns of the operand without a slot repeat the first: nobody reads their sums
-        const uint8_t *bx[NT][DOWN && !EIGHT ? 2 : 1];
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-            const int t = c * 8 + g < ns ? c * 8 + g : 0, slot = slots[s0 + t];
-            if constexpr (EIGHT) {
-                bx[c][0] = xs + t * xpitch + tig * 16;
-            } else if constexpr (DOWN) {
-                const uint8_t *hh = static_cast<const uint8_t *>(p.h);
-                bx[c][0] = hh + slot * Kb + tig * 16;
-                bx[c][1] = hh + (int64_t(n) + slot) * Kb + tig * 16;
-            } else {
-                bx[c][0] = static_cast<const uint8_t *>(p.x) + int64_t(slot / p.k) * Kb + tig * 16;
-            }
+        const int bt = g < ns ? g : 0, bslot = slots[s0 + bt];
+        const uint8_t *bx[2];  // 16 bits: x, or the two terms of h
+        uint32_t bs = 0;       // 8 bits: the row in shared memory
+        if constexpr (EIGHT) {
+            bs = uint32_t(__cvta_generic_to_shared(xs + bt * xpitch + tig * 16));
+        } else if constexpr (DOWN) {
+            const uint8_t *hh = static_cast<const uint8_t *>(p.h);
+            bx[0] = hh + bslot * Kb + tig * 16;
+            bx[1] = hh + (int64_t(n) + bslot) * Kb + tig * 16;
+        } else {
+            bx[0] = static_cast<const uint8_t *>(p.x) + int64_t(bslot / p.k) * Kb + tig * 16;
         }
-        float acc[2][NT][4];
+        float acc[2][4];
         auto clear = [&]() {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[m][c][j] = 0.f;
+                for (int j = 0; j < 4; ++j) acc[m][j] = 0.f;
         };
         auto compute = [&](const Piece<EIGHT> &b, int pc) {
-            const int64_t off = int64_t(pc) * kPiece;
+            const int off = pc * kPiece;
             if constexpr (EIGHT) {
-                float part[2][NT][4];
+                // The weights and the rows as fp16 (exactly): the tensor cores' form for warps
+                // of e4m3 is that conversion again for each of its operands.
+                float part[2][4];
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
+                for (int st = 0; st < 2; ++st) {
+                    const uint4 x = lds128(bs + off + st * 64);
 #pragma unroll
-                    for (int c = 0; c < NT; ++c)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) part[m][c][j] = 0.f;
-#pragma unroll
-                for (int st = 0; st < 2; ++st)
-#pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        if (c * 8 >= ns) continue;
-                        const uint4 x = *reinterpret_cast<const uint4 *>(bx[c][0] + off + st * 64);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 y = widen_e4m3(word(x, i));
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
-                            const uint4 u = b.a[st][2 * m], v = b.a[st][2 * m + 1];
-                            mma8<W>(part[m][c], u.x, v.x, u.y, v.y, x.x, x.y);
-                            mma8<W>(part[m][c], u.z, v.z, u.w, v.w, x.z, x.w);
+                            const uint2 u = widen_e4m3(word(b.a[st][2 * m], i));
+                            const uint2 v = widen_e4m3(word(b.a[st][2 * m + 1], i));
+                            if (st == 0 && i == 0)
+                                mma8<fp16, true>(part[m], u.x, v.x, u.y, v.y, y.x, y.y);
+                            else
+                                mma8<fp16, false>(part[m], u.x, v.x, u.y, v.y, y.x, y.y);
                         }
                     }
+                }
+                const float2 q = *reinterpret_cast<const float2 *>(sx + pc * TOK + 2 * tig);
 #pragma unroll
-                for (int c = 0; c < NT; ++c) {
-                    if (c * 8 >= ns) continue;
-                    const float2 q = *reinterpret_cast<const float2 *>(sx + pc * TOK + c * 8 + 2 * tig);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const float q0 = q.x * b.s[m], q1 = q.y * b.s[m];
-                        acc[m][c][0] = fmaf(part[m][c][0], q0, acc[m][c][0]);
-                        acc[m][c][1] = fmaf(part[m][c][1], q1, acc[m][c][1]);
-                        acc[m][c][2] = fmaf(part[m][c][2], q0, acc[m][c][2]);
-                        acc[m][c][3] = fmaf(part[m][c][3], q1, acc[m][c][3]);
-                    }
+                for (int m = 0; m < 2; ++m) {
+                    const float q0 = q.x * b.s[m], q1 = q.y * b.s[m];
+                    acc[m][0] = fmaf(part[m][0], q0, acc[m][0]);
+                    acc[m][1] = fmaf(part[m][1], q1, acc[m][1]);
+                    acc[m][2] = fmaf(part[m][2], q0, acc[m][2]);
+                    acc[m][3] = fmaf(part[m][3], q1, acc[m][3]);
                 }
             } else {
                 constexpr int TERMS = DOWN ? 2 : 1;
+                uint4 x[TERMS][2];
 #pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    const bool in = off + st * 64 + tig * 16 < Kb;
+                for (int q = 0; q < TERMS; ++q)
 #pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        if (c * 8 >= ns) continue;
-#pragma unroll
-                        for (int q = 0; q < TERMS; ++q) {
-                            uint4 x = zero4();
-                            if (in) x = *reinterpret_cast<const uint4 *>(bx[c][q] + off + st * 64);
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                const uint4 u = b.a[st][2 * m], v = b.a[st][2 * m + 1];
-                                mma8<W>(acc[m][c], u.x, v.x, u.y, v.y, x.x, x.y);
-                                mma8<W>(acc[m][c], u.z, v.z, u.w, v.w, x.z, x.w);
-                            }
-                        }
+                    for (int st = 0; st < 2; ++st) {
+                        x[q][st] = zero4();
+                        if (off + st * 64 + tig * 16 < Kb)
+                            x[q][st] = *reinterpret_cast<const uint4 *>(bx[q] + off + st * 64);
                     }
-                }
+#pragma unroll
+                for (int q = 0; q < TERMS; ++q)
+#pragma unroll
+                    for (int st = 0; st < 2; ++st)
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const uint4 u = b.a[st][2 * m], v = b.a[st][2 * m + 1];
+                            mma8<W, false>(acc[m], u.x, v.x, u.y, v.y, x[q][st].x, x[q][st].y);
+                            mma8<W, false>(acc[m], u.z, v.z, u.w, v.w, x[q][st].z, x[q][st].w);
+                        }
             }
         };
         auto finish = [&](int tl) {
             float *mine = red + (parity * kWarps + warp) * TOK * kPitch;
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mine[(c * 8 + 2 * tig + (j & 1)) * kPitch + m * 16 + g + (j >> 1) * 8] =
-                            acc[m][c][j];
+                for (int j = 0; j < 4; ++j)
+                    mine[(2 * tig + (j & 1)) * kPitch + m * 16 + g + (j >> 1) * 8] = acc[m][j];
             group_sync();
             const float *all = red + (parity * kWarps + gi * WK) * TOK * kPitch;
             parity ^= 1;
@@ -404,12 +466,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
         clear();
         // one piece is computed while the next is on its way
         auto step = [&](Piece<EIGHT> &now, Piece<EIGHT> &next) {
-            int nt = tile, npc = piece + WK;
-            if (npc >= np) {
-                npc = wk;
-                nt = tile + NG;
-            }
-            if (nt < tile1) load(next, nt, npc);
+            const int nt = ltile, npc = lpiece;
+            if (nt < tile1) load(next);
             compute(now, piece);
             if (nt != tile) {
                 finish(tile);
@@ -455,14 +513,13 @@ __global__ void __launch_bounds__(128) k_moe_few_sum(const float *__restrict__ y
     st_vec<X, 8>(f + t * C + c, o);
 }
 
-size_t few_smem(int NT, bool eight, int64_t K)
+size_t few_smem(bool eight, int64_t K)
 {
-    const int64_t nkb = fp8_blocks(K), tok = 8 * NT;
-    int64_t b = kMaxSlots * 2 + 1028 * 2 * 4 + 2 * kWarps * tok * kPitch * 4;
-    if (eight) b += tok * (nkb * kFp8Block + 64) + nkb * tok * 4;
+    const int64_t nkb = fp8_blocks(K);
+    int64_t b = kMaxSlots * 2 + 1028 * 2 * 4 + 2 * kWarps * TOK * kPitch * 4;
+    if (eight) b += TOK * (nkb * kFp8Block + 64) + nkb * TOK * 4;
     return size_t(b);
 }
-constexpr size_t kSmemMax = 232448;
 
 // How many of a block's 16 warps split a tile's k.  More of them finish a tile
 // sooner but join more often, which costs a warp about two pieces' time; fewer
@@ -488,24 +545,15 @@ int split_of(int64_t K, int bytes, int64_t tiles)
     return best;
 }
 
-template <class W, class X, int NT, bool DOWN>
+template <class W, class X, bool DOWN>
 cudaError_t launch_one(const FewP &p, cudaStream_t s)
 {
-    auto *kernel = k_moe_few<W, X, NT, DOWN>;
-    const size_t smem = few_smem(NT, sizeof(W) == 1, p.K);
+    auto *kernel = k_moe_few<W, X, DOWN>;
+    const size_t smem = few_smem(sizeof(W) == 1, p.K);
     cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kernel), int(smem));
     if (e != cudaSuccess) return e;
     MHC_PROF(DOWN ? "k_moe_few_down" : "k_moe_few_up", s);
     return launch_k(kernel, dim3(unsigned(num_sms())), dim3(kThreads), smem, s, p);
-}
-
-template <class W, class X, bool DOWN>
-cudaError_t by_columns(const FewP &p, cudaStream_t s)
-{
-    // 16 columns where an expert may have more than 8 slots and they fit
-    if (p.T > 8 && few_smem(2, sizeof(W) == 1, p.K) <= kSmemMax)
-        return launch_one<W, X, 2, DOWN>(p, s);
-    return launch_one<W, X, 1, DOWN>(p, s);
 }
 
 template <class W, class X>
@@ -518,7 +566,7 @@ cudaError_t both(FewP &p, const MoeFewArgs &a, cudaStream_t s)
     p.ntiles = int(a.F / 16);
     const int64_t segments = std::min<int64_t>(a.E, a.T * a.k);
     p.wk = split_of(p.K, sizeof(W), segments * p.ntiles);
-    cudaError_t e = by_columns<W, X, false>(p, s);
+    cudaError_t e = launch_one<W, X, false>(p, s);
     if (e != cudaSuccess) return e;
     p.wt = a.w2;
     p.s = a.s2;
@@ -526,7 +574,7 @@ cudaError_t both(FewP &p, const MoeFewArgs &a, cudaStream_t s)
     p.rows = a.C;
     p.ntiles = int((a.C + kRows - 1) / kRows);
     p.wk = split_of(p.K, sizeof(W), segments * p.ntiles);
-    e = by_columns<W, X, true>(p, s);
+    e = launch_one<W, X, true>(p, s);
     if (e != cudaSuccess) return e;
     const int64_t n = a.T * (a.C / 8);
     MHC_PROF("k_moe_few_sum", s);
