@@ -46,7 +46,7 @@ __device__ __forceinline__ float f8_up(uint32_t amax)
 }
 
 // 1 / (1 + exp(-g)): 0 where exp(-g) is inf.
-__device__ __forceinline__ float sigm(float g) { return __frcp_rn(1.f + __expf(-g)); }
+__device__ __forceinline__ float sigm(float g) { return rcp_approx(1.f + __expf(-g)); }
 // g p for p = sigm(g), 0 at -inf
 __device__ __forceinline__ float silu(float g, float p) { return p == 0.f ? 0.f : g * p; }
 
