@@ -1158,8 +1158,8 @@ void quant_args(Check &ck, mhc::Fp8QuantArgs &a, int dtype, int format, int64_t 
     format_ok(ck, format, "format");
     multiple(ck, C, 16, "C");
     if (qt || st) multiple(ck, R, 16, "R");
-    if (ck.st == MHC_OK && mhc::fp8_blocks(R) * mhc::fp8_blocks(C) > INT32_MAX)
-        ck.st = fail(MHC_ERR_BAD_SHAPE, "%s: R and C give more than 2^31 tiles", ck.fn);
+    if (ck.st == MHC_OK && R > 0 && G > INT32_MAX / (mhc::fp8_blocks(R) * mhc::fp8_blocks(C)))
+        ck.st = fail(MHC_ERR_BAD_SHAPE, "%s: G, R and C give more than 2^31 tiles", ck.fn);
     if (ck.st || G == 0 || R == 0) return;
     if (q || s) ck.ptr(q, "q").ptr(s, "s");
     if (qt || st) ck.ptr(qt, "qt").ptr(st, "st");
@@ -1174,6 +1174,7 @@ void quant_args(Check &ck, mhc::Fp8QuantArgs &a, int dtype, int format, int64_t 
     a.G = G;
     a.R = R;
     a.C = C;
+    a.nrb = unsigned(mhc::fp8_blocks(R));
     a.ncb = unsigned(mhc::fp8_blocks(C));
 }
 

@@ -27,7 +27,7 @@ struct Fp8QuantArgs {
     int64_t G, R, C;  // C: columns of the result
     int64_t F;        // swiglu: columns of gate
     int tiles;        // one scale a tile of 128 x 128
-    unsigned ncb;     // blocks of C
+    unsigned nrb, ncb;  // blocks of R and C; G times them is below 2^31
 };
 
 cudaError_t launch_fp8_quant(const Fp8QuantArgs &a, int source, int dtype, int format,

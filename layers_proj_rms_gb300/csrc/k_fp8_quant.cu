@@ -31,6 +31,14 @@ namespace mhc {
 namespace {
 
 constexpr int B = kFp8Block;
+
+// 16 bytes to shared memory, or zeros
+__device__ __forceinline__ void cp_async16(uint32_t to, const void *from, uint32_t bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                 : "memory");
+}
+
 constexpr int kRows = 4, kThreads = B / kRows * 16, kWarps = kThreads / 32;
 // What a thread holds of the tile: 4 rows x 8 columns.
 template <class T, int SRC>
@@ -40,17 +48,23 @@ struct Held {
     Vec<T, 8> w[PACKED ? kRows : 1];
     float v[PACKED ? 1 : kRows][8];
 
-    // the 8 values of row i as pairs
-    __device__ __forceinline__ void row(int i, f32x2 (&p)[4]) const
+    __device__ __forceinline__ void zero(int i)
     {
         if constexpr (PACKED) {
-            float f[8];
-            widen<T, 8>(w[i], f);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = f2_make(f[2 * k], f[2 * k + 1]);
+            zero_vec<T, 8>(w[i]);
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] = f2_make(v[i][2 * k], v[i][2 * k + 1]);
+            for (int k = 0; k < 8; ++k) v[i][k] = 0.f;
+        }
+    }
+    // the 8 values of row i
+    __device__ __forceinline__ void row(int i, float (&f)[8]) const
+    {
+        if constexpr (PACKED) {
+            widen<T, 8>(w[i], f);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = v[i][k];
         }
     }
 };
@@ -62,23 +76,27 @@ __device__ __forceinline__ uint32_t mag_bits(uint32_t h, const fp16 *)
     return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
 }
 
-// 8 values of a row: x points at them (of gate, where there are two halves), u at
-// those of up, d at the upstream gradient's.
+// Rows of 8 values that a thread reads for one of its own: gate and up, the
+// upstream gradient, gate and up.
+template <int SRC>
+constexpr int kSources = SRC == kFp8Plain ? 1 : SRC == kFp8Swiglu ? 2 : 3;
+// Whether a block walks over tiles and brings the next one to shared memory while it
+// works on this one.  16384 x 4096 in fp32 took 96 us so and 74 a block a tile, the
+// activation in fp32 85 and 66, 73664 x 4096 in bf16 220 and 238, the activation in
+// bf16 168 and 214; three sources leave no room for two blocks.
 template <class T, int SRC>
-__device__ __forceinline__ void values(Held<T, SRC> &h, int i, const T *x, const T *u, const T *d,
-                                       bool up_part)
+constexpr bool kStaged = sizeof(T) == 2 && kSources<SRC> <= 2;
+
+// The thread's row i from its 8 values of each source.
+template <class T, int SRC>
+__device__ __forceinline__ void hold(Held<T, SRC> &h, int i, const Vec<T, 8> &wg, const Vec<T, 8> &wu,
+                                     const Vec<T, 8> &wd, bool up_part)
 {
     if constexpr (Held<T, SRC>::PACKED) {
-        ld_vec<T, 8>(h.w[i], x);
+        h.w[i] = wg;
     } else if constexpr (SRC == kFp8Plain) {
-        Vec<T, 8> w;
-        ld_vec<T, 8>(w, x);
-        widen<T, 8>(w, h.v[i]);
+        widen<T, 8>(wg, h.v[i]);
     } else {
-        Vec<T, 8> wg, wu, wd;
-        ld_vec<T, 8>(wg, x);
-        if (!up_part) ld_vec<T, 8>(wu, u);
-        if constexpr (SRC == kFp8SwigluGrad) ld_vec<T, 8>(wd, d);
         float gv[8], uv[8], dv[8];
         widen<T, 8>(wg, gv);
         if constexpr (SRC == kFp8SwigluGrad) widen<T, 8>(wd, dv);
@@ -96,6 +114,37 @@ __device__ __forceinline__ void values(Held<T, SRC> &h, int i, const T *x, const
     }
 }
 
+// A thread's part of a tile: where it stands.
+template <class T, int SRC>
+struct Part {
+    int cb, rows;  // the tile's block of columns; rows that are there
+    int64_t rb, g, r0, c0;
+    bool up_part;
+    const T *x, *u, *d;  // the first row's 8 values of each source
+    int64_t step, dstep;
+
+    __device__ __forceinline__ Part(const Fp8QuantArgs &a, int halves, uint32_t t)
+    {
+        const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+        // the gate and the up tile of the same columns, which read the same rows, are neighbours
+        const uint32_t all = t / a.ncb;  // tiles are below 2^31
+        const int bx = int(t - all * a.ncb);
+        g = all / a.nrb;
+        rb = all - uint32_t(g) * a.nrb;
+        cb = halves ? (bx >> 1) + (bx & 1) * halves : bx;
+        r0 = rb * B + ty * kRows;
+        c0 = int64_t(cb) * B + tx * 8;
+        rows = c0 < a.C ? int(max(int64_t(0), min(int64_t(kRows), a.R - r0))) : 0;  // C a multiple of 8
+        up_part = SRC == kFp8SwigluGrad && c0 >= a.F;
+        step = SRC == kFp8Plain ? a.C : 2 * a.F;
+        dstep = a.F;
+        const int64_t j = up_part ? c0 - a.F : c0;
+        x = static_cast<const T *>(a.x) + (g * a.R + r0) * step + j;
+        u = x + a.F;
+        d = SRC == kFp8SwigluGrad ? static_cast<const T *>(a.da) + r0 * dstep + j : x;
+    }
+};
+
 template <class T, int FMT, int SRC, bool TILES>
 __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a, int halves)
 {
@@ -104,37 +153,72 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
     __shared__ __align__(16) uint32_t col_part[kWarps][B];
     __shared__ __align__(16) uint32_t row_m[B];
     __shared__ __align__(16) float row_up[B], col_up[B];
+    extern __shared__ __align__(16) uint8_t next[];  // [source][row][half of it][thread] 16 bytes
+    constexpr int PER = int(sizeof(T)) / 2;           // 16-byte pieces of 8 values
+    constexpr bool STAGED = kStaged<T, SRC>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tx = tid & 15, ty = tid >> 4;
-    // the gate and the up tile of the same columns, which read the same rows, are neighbours
-    const int bx = int(blockIdx.x % a.ncb);
-    const int cb = halves ? (bx >> 1) + (bx & 1) * halves : bx;
-    const int64_t rb = blockIdx.x / a.ncb, g = blockIdx.y;
-    const int64_t r0 = rb * B + ty * kRows, c0 = int64_t(cb) * B + tx * 8;
     const int64_t R = a.R, C = a.C;
-    const int64_t nrb = (R + B - 1) / B, ncb = a.ncb;
-    const bool in_c = c0 < C;  // C is a multiple of 8
-    const int rows = in_c ? int(min(int64_t(kRows), R - r0)) : 0;  // of this thread's
+    const int64_t nrb = a.nrb, ncb = a.ncb;
+    const uint32_t tiles = uint32_t(a.G) * a.nrb * a.ncb;
+    const uint32_t mine = uint32_t(__cvta_generic_to_shared(next)) + tid * 16;
+
+    // a thread brings and reads its own 16 bytes only
+    auto bring = [&](const Part<T, SRC> &q) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+                const uint32_t n = i < q.rows ? 16 : 0;
+                const uint32_t at = mine + (i * PER + k) * kThreads * 16;
+                constexpr int SLOT = kRows * PER * kThreads * 16;
+                cp_async16(at, n ? q.x + i * q.step + k * 4 : a.x, n);
+                if constexpr (SRC == kFp8Swiglu)
+                    cp_async16(at + SLOT, n ? q.u + i * q.step + k * 4 : a.x, n);
+            }
+    };
+    auto take = [&](Vec<T, 8> &w, int source, int i) {
+#pragma unroll
+        for (int k = 0; k < PER; ++k) {
+            const uint4 v = lds128(mine + ((source * kRows + i) * PER + k) * kThreads * 16);
+            w.w[4 * k] = v.x;
+            w.w[4 * k + 1] = v.y;
+            w.w[4 * k + 2] = v.z;
+            w.w[4 * k + 3] = v.w;
+        }
+    };
 
     pdl_wait();
+    Part<T, SRC> coming(a, halves, blockIdx.x);
+    if constexpr (STAGED) bring(coming);
+    // (a block a tile where nothing is staged)
+    for (uint32_t t = blockIdx.x; t < tiles; t = STAGED ? t + gridDim.x : tiles) {
+    const Part<T, SRC> part = coming;
+    const int cb = part.cb, rows = part.rows;
+    const int64_t rb = part.rb, g = part.g, r0 = part.r0, c0 = part.c0;
     H held;
-    {
-        const bool up_part = SRC == kFp8SwigluGrad && c0 >= a.F;
-        const int64_t step = SRC == kFp8Plain ? C : 2 * a.F, j = up_part ? c0 - a.F : c0;
-        const T *x = static_cast<const T *>(a.x) + (g * R + r0) * step + j;
-        const T *d = SRC == kFp8SwigluGrad ? static_cast<const T *>(a.da) + r0 * a.F + j : nullptr;
+    if constexpr (STAGED) asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (i < rows) {
-                values<T, SRC>(held, i, x + i * step, x + i * step + a.F, d + i * a.F, up_part);
-            } else if constexpr (H::PACKED) {
-                zero_vec<T, 8>(held.w[i]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) held.v[i][k] = 0.f;
-            }
+    for (int i = 0; i < kRows; ++i) {
+        Vec<T, 8> wg, wu, wd;
+        if constexpr (STAGED) {
+            take(wg, 0, i);
+            if constexpr (SRC == kFp8Swiglu) take(wu, 1, i);
+            hold<T, SRC>(held, i, wg, wu, wd, part.up_part);
+        } else if (i < rows) {
+            ld_vec<T, 8>(wg, part.x + i * part.step);
+            if (SRC != kFp8Plain && !part.up_part) ld_vec<T, 8>(wu, part.u + i * part.step);
+            if (SRC == kFp8SwigluGrad) ld_vec<T, 8>(wd, part.d + i * part.dstep);
+            hold<T, SRC>(held, i, wg, wu, wd, part.up_part);
+        } else {
+            held.zero(i);
         }
     }
+    if constexpr (STAGED)
+        if (t + gridDim.x < tiles) {
+            coming = Part<T, SRC>(a, halves, t + gridDim.x);
+            bring(coming);
+        }
     if (a.y) {
         T *y = static_cast<T *>(a.y) + (g * R + r0) * C + c0;
 #pragma unroll
@@ -146,30 +230,31 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
                     st_vec<T, 8>(y + i * C, w);
                 }
             }
-        if (!a.q && !a.qt) return;
+        if (!a.q && !a.qt) continue;
     }
 
     // the largest magnitudes: of the thread's rows and columns, then of the lanes'
     uint32_t rm[kRows], cm[8];
     if constexpr (H::PACKED) {
-        uint32_t c2[4] = {0, 0, 0, 0}, r2[kRows];
+        uint32_t c2[4] = {0, 0, 0, 0}, r2[kRows], last[4];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            uint32_t m = 0;
+            uint32_t r4[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const uint32_t x = held.w[i].w[k] & 0x7fff7fffu;
-                m = __vmaxu2(m, x);
-                c2[k] = __vmaxu2(c2[k], x);
+                r4[k] = held.w[i].w[k] & 0x7fff7fffu;
+                if (i % 2) c2[k] = __vimax3_u16x2(c2[k], last[k], r4[k]);
+                last[k] = r4[k];
             }
+            const uint32_t m = __vimax3_u16x2(__vimax3_u16x2(r4[0], r4[1], r4[2]), r4[3], 0);
             r2[i] = max(m & 0xffffu, m >> 16);
         }
         if (a.q && !TILES) {  // two rows a word
             uint32_t p = r2[0] | r2[1] << 16, q = r2[2] | r2[3] << 16;
 #pragma unroll
             for (int d = 8; d > 0; d >>= 1) {
-                p = __vmaxu2(p, __shfl_xor_sync(kFull, p, d));
-                q = __vmaxu2(q, __shfl_xor_sync(kFull, q, d));
+                p = __vimax3_u16x2(p, __shfl_xor_sync(kFull, p, d), 0);
+                q = __vimax3_u16x2(q, __shfl_xor_sync(kFull, q, d), 0);
             }
             r2[0] = p & 0xffffu;
             r2[1] = p >> 16;
@@ -181,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
         if (a.qt && !TILES) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                c2[k] = __vmaxu2(c2[k], __shfl_xor_sync(kFull, c2[k], 16));
+                c2[k] = __vimax3_u16x2(c2[k], __shfl_xor_sync(kFull, c2[k], 16), 0);
                 cm[2 * k] = mag_bits(c2[k] & 0xffffu, static_cast<const T *>(nullptr));
                 cm[2 * k + 1] = mag_bits(c2[k] >> 16, static_cast<const T *>(nullptr));
             }
@@ -259,44 +344,43 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             if (i < rows) {
-                f32x2 p[4];
-                held.row(i, p);
                 float f[8];
-                const f32x2 m = f2_make(up[i], up[i]);
+                held.row(i, f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) f2_split(f2_mul(p[k], m), f[2 * k], f[2 * k + 1]);
+                for (int k = 0; k < 8; ++k) f[k] *= up[i];
                 *reinterpret_cast<uint2 *>(q + i * C) =
                     make_uint2(f8_cvt4<FMT>(f[0], f[1], f[2], f[3]), f8_cvt4<FMT>(f[4], f[5], f[6], f[7]));
             }
         }
     }
-    if (!a.qt) return;
-    float t[kRows][8];  // the columns' values
+    if (!a.qt) {
+        __syncthreads();
+        continue;
+    }
+    float tc[kRows][8];  // the columns' values
     {
-        f32x2 cu[4];
+        float cu[8];
         if (TILES) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) cu[k] = f2_make(up_tile, up_tile);
+            for (int k = 0; k < 8; ++k) cu[k] = up_tile;
         } else {
             const float4 x = *reinterpret_cast<const float4 *>(&col_up[tx * 8]);
             const float4 y = *reinterpret_cast<const float4 *>(&col_up[tx * 8 + 4]);
-            cu[0] = f2_make(x.x, x.y);
-            cu[1] = f2_make(x.z, x.w);
-            cu[2] = f2_make(y.x, y.y);
-            cu[3] = f2_make(y.z, y.w);
+            const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k) cu[k] = z[k];
         }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            f32x2 p[4];
-            held.row(i, p);
+            held.row(i, tc[i]);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) f2_split(f2_mul(p[k], cu[k]), t[i][2 * k], t[i][2 * k + 1]);
+            for (int k = 0; k < 8; ++k) tc[i][k] *= cu[k];
         }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j)  // column tx*8 + j, rows ty*4 .. ty*4 + 3
         *reinterpret_cast<uint32_t *>(tile + (tx * 8 + j) * B + (ty ^ (2 * tx)) * 4) =
-            f8_cvt4<FMT>(t[0][j], t[1][j], t[2][j], t[3][j]);
+            f8_cvt4<FMT>(tc[0][j], tc[1][j], tc[2][j], tc[3][j]);
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < B * 8 / kThreads; ++k) {
@@ -307,26 +391,34 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
         if (col < C && row < R)  // R is a multiple of 16
             *reinterpret_cast<uint4 *>(a.qt + (g * C + col) * R + row) = w;
     }
+    }
+}
+
+template <class T, int FMT, int SRC, bool TILES>
+cudaError_t run(const Fp8QuantArgs &a, const char *name, cudaStream_t s)
+{
+    auto *kernel = k_fp8_quant<T, FMT, SRC, TILES>;
+    const int smem = kStaged<T, SRC> ? kSources<SRC> * kRows * int(sizeof(T)) * 8 * kThreads : 0;
+    if (smem) {
+        cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kernel), smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int halves = SRC == kFp8SwigluGrad && a.F % B == 0 ? int(a.F / B) : 0;
+    // two blocks an SM that walk over the tiles, or a block a tile
+    int64_t blocks = a.G * a.nrb * a.ncb;
+    if (kStaged<T, SRC>) blocks = std::min<int64_t>(blocks, 2 * num_sms());
+    MHC_PROF(name, s);
+    return launch_k(kernel, dim3(unsigned(blocks)), dim3(kThreads), smem, s,
+                    a, halves);
 }
 
 template <class T, int FMT>
 cudaError_t by_source(const Fp8QuantArgs &a, int source, cudaStream_t s)
 {
-    const dim3 grid{unsigned(a.ncb * fp8_blocks(a.R)), unsigned(a.G)};
-    const int halves = source == kFp8SwigluGrad && a.F % B == 0 ? int(a.F / B) : 0;
-    if (source == kFp8Swiglu) {
-        MHC_PROF("k_fp8_swiglu_fwd", s);
-        return launch_k(k_fp8_quant<T, FMT, kFp8Swiglu, false>, grid, dim3(kThreads), 0, s, a, halves);
-    }
-    if (source == kFp8SwigluGrad) {
-        MHC_PROF("k_fp8_swiglu_bwd", s);
-        return launch_k(k_fp8_quant<T, FMT, kFp8SwigluGrad, false>, grid, dim3(kThreads), 0, s, a,
-                        halves);
-    }
-    MHC_PROF("k_fp8_quant", s);
-    if (a.tiles)
-        return launch_k(k_fp8_quant<T, FMT, kFp8Plain, true>, grid, dim3(kThreads), 0, s, a, halves);
-    return launch_k(k_fp8_quant<T, FMT, kFp8Plain, false>, grid, dim3(kThreads), 0, s, a, halves);
+    if (source == kFp8Swiglu) return run<T, FMT, kFp8Swiglu, false>(a, "k_fp8_swiglu_fwd", s);
+    if (source == kFp8SwigluGrad) return run<T, FMT, kFp8SwigluGrad, false>(a, "k_fp8_swiglu_bwd", s);
+    return a.tiles ? run<T, FMT, kFp8Plain, true>(a, "k_fp8_quant", s)
+                   : run<T, FMT, kFp8Plain, false>(a, "k_fp8_quant", s);
 }
 
 template <class T>
