@@ -56,7 +56,7 @@ struct GemmCfg {
     static constexpr int CG = CG_, BN = BN_;
     static_assert(BN == 128 * CG, "each CTA loads 128 rows of B");
     static constexpr int A_BYTES = BM * BK, B_BYTES = 128 * BK, STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = 4;
+    static constexpr int STAGES = CG == 1 ? 5 : 4;
     static constexpr int SC = 6;     // blocks whose scales are there or in flight
     static constexpr int AHEAD = 4;  // of them in flight at most; two are being read
     static constexpr int SC_FLOATS = BM + BN;
@@ -556,11 +556,11 @@ __global__ void __launch_bounds__(P::THREADS, 1)
             // the MMAs, the second's pass that word on.  After a fault they only keep the
             // barriers going.
             const int b = warp >> 1;
-            static_assert(P::STAGES % 2 == 0, "a warp's blocks are every second stage");
             const uint64_t da0 = tc::desc_kmajor_sw128(tc::smem_u32(smem));
             const uint64_t db0 = tc::desc_kmajor_sw128(tc::smem_u32(smem) + P::A_BYTES);
             const uint32_t d0 = tmem + b * P::BN;
             int st = b, done = 0;       // stage; blocks of this warp so far
+            int gone = 0;               // those that are read
             uint32_t ph = 0, aph = 1;   // phases of the stage's and the accumulator's barrier
             bool ok = true;
             auto collect = [&]() {  // this warp's oldest block: accumulator and scales are read
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
                         tc::tc_fence_before();
                         arrive_first(&acc_empty[b]);
                     }
-                    collected[b] = collected[b] + 1;
+                    collected[b] = ++gone;
                 }
             };
             int par = b;  // the first block of the next tile that is this warp's
