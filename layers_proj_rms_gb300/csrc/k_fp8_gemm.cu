@@ -14,26 +14,27 @@
 // registers, so scales of any value are exact to fp32 and the long sum is
 // rounded to nearest, once a block.
 //
-// What bounds it: one CTA's MMA of 128 x 256 x 32 reads 12 KB of shared memory
-// and its TMA loads write as much, 1.5 times what the SM can do while the MMA
-// runs (measured: 855 cycles a block of 128, of 512 for the products).  So two
-// CTAs share a tile of 256 x 256 (cta_group::2), each with its 128 rows of A and
-// half of B: 32 KB in and 32 KB out for the same 512 cycles.  Where the segments
-// are short (below 160 rows on average a pair would work on empty rows) a CTA
-// takes tiles of 128 x 128 by itself: there the weights' way through HBM is what
-// counts, and a stage is 32 KB all the same.
+// What bounds it: an MMA of 128 x 256 x 32 reads 12 KB of shared memory and its
+// TMA loads write as much; a block of 128 takes 855 cycles, of 512 for the products,
+// and with every SM at work the GPU is at its power limit besides.  Tiles of 128 x 256
+// move 1.5 times the products per byte of 128 x 128 (65536 rows of 64 experts, K 4096,
+// 4096 columns: 1007-1081 us of 1289-1330) and are taken where enough of them fill the
+// SMs; the rule and its measurements stand at wide_sooner().  Two CTAs that share a
+// tile of 256 x 256, each with half of B (cta_group::2, 32 KB in and out for the same
+// products), were 1086 us of 1081, 955 of 925 for weights: the waits across the pair
+// take what the feed gains, so there are no pairs.
 //
-// A CTA is persistent, one an SM: a warp that brings the operands (TMA) and the
-// scales (cp.async), two that issue the MMAs of the even and the odd blocks (the
-// first CTA's of a pair), one that waits for them, and eight epilogue warps, in a
-// pair sixteen, each 32 rows x 64 columns.  Results leave
-// through a 4 KB box of shared memory a warp (32 rows x 128 bytes) by TMA store, so
-// the next tile's blocks do not wait for them; a box that the segment's end cuts
-// is copied row by row.
+// A CTA is persistent, one an SM: a warp that brings the operands (TMA), two that
+// issue the MMAs of the even and the odd blocks, one that brings the scales
+// (cp.async) and waits for the products, and eight epilogue warps, with 256 columns
+// sixteen, each 32 rows x 64 columns.  (The scales by the operands' warp: 1089 us
+// of 1081, 963 of 926 with weights; its own loop is what feeds the MMAs.)  Results
+// leave through a 4 KB box of shared memory a warp (32 rows x 128 bytes) by TMA
+// store, so the next tile's blocks do not wait for them; a box that the segment's
+// end cuts is copied row by row.
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "elem.cuh"
 #include "fp8.h"
@@ -50,13 +51,13 @@ constexpr int BM = 128, BK = 128;
 // Fault codes of bad offsets in device memory.
 enum : int { kFaultOffsets = 205, kFaultOffsetsAlign = 206 };
 
-// CG CTAs share a tile of 128 CG x BN; each loads 128 rows of A and of B a block.
-template <int CG_, int BN_>
+// Tiles of 128 x BN.
+template <int BN_>
 struct GemmCfg {
-    static constexpr int CG = CG_, BN = BN_;
-    static_assert(BN == 128 * CG, "each CTA loads 128 rows of B");
-    static constexpr int A_BYTES = BM * BK, B_BYTES = 128 * BK, STAGE = A_BYTES + B_BYTES;
-    static constexpr int STAGES = CG == 1 ? 5 : 4;
+    static constexpr int BN = BN_;
+    static constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
+    static constexpr int STAGES = BN == 128 ? 5 : 3;
+    static constexpr bool SPLIT = BN == 256;  // registers go to the epilogue
     static constexpr int SC = 6;     // blocks whose scales are there or in flight
     static constexpr int AHEAD = 4;  // of them in flight at most; two are being read
     static constexpr int SC_FLOATS = BM + BN;
@@ -83,99 +84,23 @@ struct GemmP {
     int64_t N;
     int G, R;            // segments, sorted rows
     int nkb;             // rows: blocks of K
-    int mt, nt;          // tiles of M (weights) and N, of a pair where there are two CTAs
+    int mt, nt;          // tiles of M (weights) and N
     uint32_t idesc;
     void *out;
     int *fault;
 };
 
-template <int CG>
 __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                        uint32_t idesc, uint32_t accumulate)
 {
-    if constexpr (CG == 1)
-        asm volatile(
-            "{\n"
-            ".reg .pred p;\n"
-            "setp.ne.b32 p, %4, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-            "}\n" ::"r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n"
-            ".reg .pred p;\n"
-            "setp.ne.b32 p, %4, 0;\n"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
-            "}\n" ::"r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
-}
-
-// Arrives on `bar`, in a pair on both CTAs' barriers at that place, when all
-// earlier MMAs of this thread are complete.
-template <int CG>
-__device__ __forceinline__ void commit(uint64_t *bar)
-{
-    if constexpr (CG == 1)
-        tc::mma_commit(bar);
-    else
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-            " [%0], %1;" ::"r"(tc::smem_u32(bar)),
-            "h"(uint16_t(3))
-            : "memory");
-}
-
-template <int CG>
-__device__ __forceinline__ void tmem_alloc(uint32_t *dst, uint32_t ncols)
-{
-    if constexpr (CG == 1) {
-        tc::tmem_alloc(dst, ncols);
-    } else {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         tc::smem_u32(dst)),
-                     "r"(ncols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    }
-}
-template <int CG>
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols)
-{
-    if constexpr (CG == 1)
-        tc::tmem_dealloc(taddr, ncols);
-    else
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                     : "memory");
-}
-
-__device__ __forceinline__ uint32_t cta_rank()
-{
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// The shared::cluster address of the first CTA's copy of what stands at p here.
-__device__ __forceinline__ uint32_t of_first(const void *p)
-{
-    uint32_t r;
-    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(tc::smem_u32(p)));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n"
-                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// An arrival on a barrier of the first CTA.  What it orders is reads of TMEM, which
-// have ended before it (tcgen05.wait::ld), no writes to memory: with a release at
-// cluster scope, a fence of all the warp's memory operations, the epilogue took 1680
-// cycles a block, of 500.
-__device__ __forceinline__ void arrive_first(const uint64_t *bar)
-{
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(of_first(bar)) : "memory");
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // Named barriers: block i's products are there (a group of epilogue warps and the
@@ -188,39 +113,23 @@ __device__ __forceinline__ void bar_arrive(int id, int count)
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// TMA loads into this CTA's shared memory; a pair's complete on a barrier of the first CTA.
-template <int CG>
+// TMA loads by shared-memory addresses
 __device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *m, int x, int y, uint32_t bar)
 {
-    if constexpr (CG == 1)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
-            : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
-template <int CG>
 __device__ __forceinline__ void load_3d(uint32_t dst, const CUtensorMap *m, int x, int y, int z,
                                         uint32_t bar)
 {
-    if constexpr (CG == 1)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
-            : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 
 __device__ __forceinline__ void store_2d(const CUtensorMap *m, uint32_t src, int x, int y)
@@ -283,8 +192,7 @@ struct Tile {
 // Tiles of an expert go down the rows first, in groups of 16 row tiles: the
 // CTAs that run at one time then share both operands' tiles in L2.
 template <class P, bool W>
-__device__ __forceinline__ Tile tile_of(const GemmP &p, const int *seg, const int *first, int t,
-                                        int rank)
+__device__ __forceinline__ Tile tile_of(const GemmP &p, const int *seg, const int *first, int t)
 {
     Tile x;
     int local, mt;
@@ -310,12 +218,12 @@ __device__ __forceinline__ Tile tile_of(const GemmP &p, const int *seg, const in
     const int m = 16 * g + rem % ms;
     x.n0 = rem / ms * P::BN;
     if (W) {
-        x.row0 = (m * P::CG + rank) * BM;
+        x.row0 = m * BM;
         x.row_end = int(p.out_rows);
         x.kb0 = seg[x.e] / BK;
         x.nkb = (seg[x.e + 1] - seg[x.e] + BK - 1) / BK;
     } else {
-        x.row0 = seg[x.e] + (m * P::CG + rank) * BM;
+        x.row0 = seg[x.e] + m * BM;
         x.row_end = seg[x.e + 1];
         x.kb0 = 0;
         x.nkb = p.nkb;
@@ -343,14 +251,13 @@ struct Cursor {
     int t, tstep, ntiles, left;  // tile; blocks of it that are left, 0 at the end
 
     __device__ __forceinline__ Cursor(const GemmP &p, const int *seg, const int *first, int t0,
-                                      int step, int nt, int rank, int lane)
+                                      int step, int nt, int lane)
         : row(nullptr), col(nullptr), row_step(0), col_step(0), in(0), t(t0 - step), tstep(step),
           ntiles(nt), left(1)
     {
-        next(p, seg, first, rank, lane);
+        next(p, seg, first, lane);
     }
-    __device__ __forceinline__ void next(const GemmP &p, const int *seg, const int *first, int rank,
-                                         int lane)
+    __device__ __forceinline__ void next(const GemmP &p, const int *seg, const int *first, int lane)
     {
         row += row_step;
         col += col_step;
@@ -358,7 +265,7 @@ struct Cursor {
         do {
             t += tstep;
             if (t >= ntiles) return;
-            const Tile x = tile_of<P, W>(p, seg, first, t, rank);
+            const Tile x = tile_of<P, W>(p, seg, first, t);
             left = x.nkb;
             const int64_t r0 = int64_t(x.kb0) * p.out_rows + x.row0;
             // all 128 rows by 16 bytes a lane, where they and the step are so aligned
@@ -414,7 +321,6 @@ __global__ void __launch_bounds__(P::THREADS, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tma, const __grid_constant__ CUtensorMap tmb,
                const __grid_constant__ CUtensorMap tmo, const GemmP p)
 {
-    constexpr int CG = P::CG;
     pdl_wait();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -425,22 +331,17 @@ __global__ void __launch_bounds__(P::THREADS, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + P::OFF_BAR);
     uint64_t *empty = full + P::STAGES;
     uint64_t *acc_full = empty + P::STAGES;
-    uint64_t *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 2);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 2);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
     volatile int *collected = abort_flag + 1;  // [2] even, odd blocks: one past the last one read
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = CG == 1 ? 0 : int(cta_rank());
     if (threadIdx.x == 0) {
         for (int s = 0; s < P::STAGES; ++s) {
             tc::mbar_init(&full[s], 1);
             tc::mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) {
-            tc::mbar_init(&acc_full[b], 1);
-            tc::mbar_init(&acc_empty[b], 1);
-        }
+        for (int b = 0; b < 2; ++b) tc::mbar_init(&acc_full[b], 1);
         *abort_flag = 0;
         collected[0] = collected[1] = 0;
         tc::fence_barrier_init();
@@ -448,7 +349,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
         tc::tma_prefetch_desc(&tmb);
         tc::tma_prefetch_desc(&tmo);
     }
-    if (warp == 1) tmem_alloc<CG>(tmem_slot, P::TMEM_COLS);
+    if (warp == 1) tc::tmem_alloc(tmem_slot, P::TMEM_COLS);
     // The segments: offsets that go back, leave the rows or (weights) stand off
     // the blocks are moved to the nearest that do not, and reported.
     for (int e = threadIdx.x; e <= p.G; e += P::THREADS)
@@ -476,7 +377,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
             // row tiles of segment e - 1 before v
             int prev = __shfl_up_sync(kFull, v, 1);
             if (lane == 0) prev = e0 == 0 ? v : carry;
-            int n = e <= p.G && e > 0 ? (v - prev + CG * BM - 1) / (CG * BM) : 0;
+            int n = e <= p.G && e > 0 ? (v - prev + BM - 1) / BM : 0;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int o = __shfl_up_sync(kFull, n, d);
@@ -490,16 +391,15 @@ __global__ void __launch_bounds__(P::THREADS, 1)
     }
     tc::tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();  // the other CTA's barriers are there
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     const int ntiles = W ? p.G * p.mt * p.nt : first[p.G] * p.nt;
-    const int t0 = blockIdx.x / CG, tstep = gridDim.x / CG;
+    const int t0 = blockIdx.x, tstep = gridDim.x;
 
-    // In a pair registers go from the four issuing warps to the epilogue, which
+    // With 256 columns registers go from the four issuing warps to the epilogue, which
     // holds the sums: 128 * 64 + 512 * 104 = 640 * 96, what the block was launched with.
     if (warp < 4) {
-        if constexpr (CG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if constexpr (P::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         // These loops run beside the epilogue's warps, at five cycles and more an
         // instruction: a hundred instructions a block would be the products' time, so
         // what changes from block to block is stepped, not computed.
@@ -508,22 +408,20 @@ __global__ void __launch_bounds__(P::THREADS, 1)
                 int st = 0, left = 0;  // stage; loads that nothing has waited for
                 uint32_t ph = 1;       // a barrier's phase before its first counts as complete
                 const uint32_t smem0 = tc::smem_u32(smem), bar0 = tc::smem_u32(full);
-                const uint32_t to0 = CG == 1 ? bar0 : of_first(full);
                 bool ok = true;
                 for (int t = t0; t < ntiles && ok; t += tstep) {
-                    const Tile x = tile_of<P, W>(p, seg, first, t, rank);
-                    const int brow = x.n0 + rank * 128;
+                    const Tile x = tile_of<P, W>(p, seg, first, t);
                     int k = x.kb0 * BK;
                     for (int kb = 0; kb < x.nkb; ++kb, k += BK) {
                         ok = tc::mbar_wait(&empty[st], ph, p.fault, tc::kFaultTimeoutEmpty);
                         if (!ok) break;
-                        const uint32_t a = smem0 + st * P::STAGE, bar = to0 + st * 8;
-                        if (rank == 0) tc::mbar_arrive_expect_tx(&full[st], CG * P::STAGE);
-                        load_2d<CG>(a, &tma, k, x.row0, bar);
+                        const uint32_t a = smem0 + st * P::STAGE, bar = bar0 + st * 8;
+                        tc::mbar_arrive_expect_tx(&full[st], P::STAGE);
+                        load_2d(a, &tma, k, x.row0, bar);
                         if (W)
-                            load_2d<CG>(a + P::A_BYTES, &tmb, k, brow, bar);
+                            load_2d(a + P::A_BYTES, &tmb, k, x.n0, bar);
                         else
-                            load_3d<CG>(a + P::A_BYTES, &tmb, k, brow, x.e, bar);
+                            load_3d(a + P::A_BYTES, &tmb, k, x.n0, x.e, bar);
                         left = min(left + 1, P::STAGES);
                         if (++st == P::STAGES) {
                             st = 0;
@@ -549,45 +447,30 @@ __global__ void __launch_bounds__(P::THREADS, 1)
             }
             __syncwarp();
         } else if (warp != 2) {
-            // Two warps take the even and the odd blocks, each with its accumulator: while one's
-            // MMAs run the other goes through its waits, 100 cycles and more each beside the
-            // tensor cores' own traffic (one warp alone: 640 of 1420 cycles a block).  Each
-            // collects the epilogue's word that its accumulator is read; the first CTA's issue
-            // the MMAs, the second's pass that word on.  After a fault they only keep the
-            // barriers going.
+            // Two warps issue the MMAs of the even and the odd blocks, each with its accumulator:
+            // while one's run the other goes through its waits, 100 cycles and more each beside
+            // the tensor cores' own traffic (one warp alone spent 640 of 1420 cycles a block
+            // on them).  After a fault they only keep the barriers going.
             const int b = warp >> 1;
             const uint64_t da0 = tc::desc_kmajor_sw128(tc::smem_u32(smem));
             const uint64_t db0 = tc::desc_kmajor_sw128(tc::smem_u32(smem) + P::A_BYTES);
             const uint32_t d0 = tmem + b * P::BN;
             int st = b, done = 0;       // stage; blocks of this warp so far
             int gone = 0;               // those that are read
-            uint32_t ph = 0, aph = 1;   // phases of the stage's and the accumulator's barrier
+            uint32_t ph = 0;            // phase of the stage's barrier
             bool ok = true;
             auto collect = [&]() {  // this warp's oldest block: accumulator and scales are read
                 tc::named_bar_sync(bar_read(b), 32 * (P::EPI_WARPS + 1));
-                if (lane == 0) {
-                    if (rank) {
-                        tc::tc_fence_after();
-                        tc::tc_fence_before();
-                        arrive_first(&acc_empty[b]);
-                    }
-                    collected[b] = ++gone;
-                }
+                if (lane == 0) collected[b] = ++gone;
             };
             int par = b;  // the first block of the next tile that is this warp's
             for (int t = t0; t < ntiles; t += tstep) {
                 const int nkb = blocks_of<W>(p, seg, t);
                 int kb = par;
                 for (; kb < nkb; kb += 2, ++done) {
-                    if (rank) {
-                        collect();
-                        continue;
-                    }
                     if (done) collect();
                     if (lane == 0 && ok) {
-                        ok = tc::mbar_wait(&full[st], ph, p.fault, tc::kFaultTimeoutFull) &&
-                             (CG == 1 ||
-                              tc::mbar_wait(&acc_empty[b], aph, p.fault, tc::kFaultTimeoutAcc));
+                        ok = tc::mbar_wait(&full[st], ph, p.fault, tc::kFaultTimeoutFull);
                         if (!ok) *abort_flag = 1;
                     }
                     if (lane == 0 && ok) {
@@ -595,11 +478,10 @@ __global__ void __launch_bounds__(P::THREADS, 1)
                         const uint64_t da = da0 + st * (P::STAGE >> 4), db = db0 + st * (P::STAGE >> 4);
 #pragma unroll
                         for (int kk = 0; kk < BK / 32; ++kk)
-                            mma_f8<CG>(d0, da + 2 * kk, db + 2 * kk, p.idesc, kk > 0);
-                        commit<CG>(&empty[st]);
-                        commit<CG>(&acc_full[b]);
+                            mma_f8(d0, da + 2 * kk, db + 2 * kk, p.idesc, kk > 0);
+                        tc::mma_commit(&empty[st]);
+                        tc::mma_commit(&acc_full[b]);
                     }
-                    aph ^= 1;
                     st += 2;
                     if (st >= P::STAGES) {
                         st -= P::STAGES;
@@ -609,12 +491,12 @@ __global__ void __launch_bounds__(P::THREADS, 1)
                 }
                 par = kb - nkb;
             }
-            if (rank == 0 && done) collect();
+            if (done) collect();
         } else {
             // Brings each block's scales, AHEAD blocks before they are read, and waits for the
             // products and the scales for the epilogue: one warp at the barriers in shared
             // memory, which the tensor cores keep busy, not sixteen.
-            Cursor<P, W> c(p, seg, first, t0, tstep, ntiles, rank, lane);
+            Cursor<P, W> c(p, seg, first, t0, tstep, ntiles, lane);
             const uint32_t ring = tc::smem_u32(scales);
             uint32_t slot = 0;
             int ahead = 0;  // blocks whose scales are brought and not yet passed on
@@ -625,7 +507,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
                     c.load(p, ring + slot);
                     slot = slot == (P::SC - 1) * P::SC_FLOATS * 4 ? 0 : slot + P::SC_FLOATS * 4;
                     ++ahead;
-                    c.next(p, seg, first, rank, lane);
+                    c.next(p, seg, first, lane);
                 }
                 if (ahead == 0) break;
                 if (ahead == P::AHEAD)
@@ -651,7 +533,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
             }
         }
     } else {
-        if constexpr (CG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        if constexpr (P::SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int q = warp & 3, h = (warp - 4) >> 2;
         const int g = lane >> 2, tig = lane & 3;
         const uint32_t trow = tmem + (uint32_t(q * 32) << 16) + h * P::COLS;
@@ -661,7 +543,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
         uint32_t slot = 0;
         int b = 0;
         for (int t = t0; t < ntiles; t += tstep) {
-            const Tile x = tile_of<P, W>(p, seg, first, t, rank);
+            const Tile x = tile_of<P, W>(p, seg, first, t);
             // rows: acc[c], row q*32 + lane, column c;  weights: acc[16 n + v], fragment v
             // (tmem_ld16x32) of rows 16 (n % 2), columns 32 (n / 2)
             float acc[P::COLS];
@@ -811,29 +693,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
     }
     tc::tc_fence_before();
     __syncthreads();
-    if constexpr (CG == 2) cluster_sync();  // nothing of the other CTA's reaches in here any more
-    if (warp == 1) tmem_dealloc<CG>(tmem, P::TMEM_COLS);
-}
-
-// CTAs (a multiple of CG) that run at one time, one an SM.
-template <int CG, class K>
-cudaError_t resident(K *kernel, int threads, int smem, int64_t *ctas)
-{
-    *ctas = num_sms();
-    if (CG == 1) return cudaSuccess;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(*ctas / CG * CG));
-    cfg.blockDim = dim3(unsigned(threads));
-    cfg.dynamicSmemBytes = size_t(smem);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {CG, 1, 1};
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-    *ctas = int64_t(n > 0 ? n : 1) * CG;
-    return e;
+    if (warp == 1) tc::tmem_dealloc(tmem, P::TMEM_COLS);
 }
 
 template <class P, bool W, class O>
@@ -843,29 +703,17 @@ cudaError_t run(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap 
     auto *kernel = k_fp8_gemm<P, W, O>;
     cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kernel), P::SMEM);
     if (e != cudaSuccess) return e;
-    static std::atomic<int64_t> known[64];  // by device
-    int dev = 0;
-    e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    int64_t ctas = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
-    if (ctas == 0) {
-        e = resident<P::CG>(kernel, P::THREADS, P::SMEM, &ctas);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) known[dev].store(ctas, std::memory_order_relaxed);
-    }
     MHC_PROF(W ? "k_fp8_wgrad" : "k_fp8_gemm", s);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min(ctas, std::max<int64_t>(tiles, 1) * P::CG)));
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(num_sms(), std::max<int64_t>(tiles, 1))));
     cfg.blockDim = dim3(P::THREADS);
     cfg.dynamicSmemBytes = P::SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute attr[2];
+    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim = {P::CG, 1, 1};
     cfg.attrs = attr;
-    cfg.numAttrs = P::CG == 1 ? 1 : 2;
+    cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, ta, tb, to, p);
 }
 
@@ -878,8 +726,8 @@ cudaError_t by_type(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensor
     return run<P, W, float>(ta, tb, to, p, tiles, s);
 }
 
-typedef GemmCfg<1, 128> One;
-typedef GemmCfg<2, 256> Pair;
+typedef GemmCfg<128> Narrow;
+typedef GemmCfg<256> Wide;
 
 template <class P>
 cudaError_t gemm_rows(const Fp8GemmArgs &a, int out_dtype, cudaStream_t s)
@@ -894,7 +742,7 @@ cudaError_t gemm_rows(const Fp8GemmArgs &a, int out_dtype, cudaStream_t s)
     p.R = int(a.R);
     p.nkb = int(fp8_blocks(a.K));
     p.nt = int((a.N + P::BN - 1) / P::BN);
-    p.idesc = idesc_f8_f32(a.fa, a.fb, P::CG * BM, P::BN);
+    p.idesc = idesc_f8_f32(a.fa, a.fb, BM, P::BN);
     p.out = a.out;
     p.fault = a.fault;
     CUtensorMap ta, tb, to;
@@ -903,12 +751,12 @@ cudaError_t gemm_rows(const Fp8GemmArgs &a, int out_dtype, cudaStream_t s)
     const uint64_t db[3] = {uint64_t(a.K), uint64_t(a.N), uint64_t(a.G)};
     const uint64_t rb[2] = {uint64_t(a.K), uint64_t(a.K) * uint64_t(a.N)};
     const uint64_t dn[2] = {uint64_t(a.N), uint64_t(a.R)}, rn[1] = {uint64_t(a.N) * es};
-    const uint32_t ba[2] = {BK, BM}, bb[3] = {BK, 128, 1}, bo[2] = {uint32_t(128 / es), 32};
+    const uint32_t ba[2] = {BK, BM}, bb[3] = {BK, P::BN, 1}, bo[2] = {uint32_t(128 / es), 32};
     if (!tmap_u8(&ta, a.a, 2, da, ra, ba) || !tmap_u8(&tb, a.b, 3, db, rb, bb) ||
         !tmap_out(&to, a.out, out_dtype, 2, dn, rn, bo))
         return cudaErrorInvalidValue;
     // a bound on the tiles: every segment may end inside one
-    const int64_t tiles = (a.R / (P::CG * BM) + std::min(a.G, a.R)) * p.nt;
+    const int64_t tiles = (a.R / BM + std::min(a.G, a.R)) * p.nt;
     return by_type<P, false>(ta, tb, to, p, tiles, out_dtype, s);
 }
 
@@ -923,9 +771,9 @@ cudaError_t gemm_weights(const Fp8WgradArgs &a, int out_dtype, cudaStream_t s)
     p.N = a.N;
     p.G = int(a.G);
     p.R = int(a.R);
-    p.mt = int((a.M + P::CG * BM - 1) / (P::CG * BM));
+    p.mt = int((a.M + BM - 1) / BM);
     p.nt = int((a.N + P::BN - 1) / P::BN);
-    p.idesc = idesc_f8_f32(a.fa, a.fb, P::CG * BM, P::BN);
+    p.idesc = idesc_f8_f32(a.fa, a.fb, BM, P::BN);
     p.out = a.out;
     p.fault = a.fault;
     CUtensorMap ta, tb, to;
@@ -934,23 +782,45 @@ cudaError_t gemm_weights(const Fp8WgradArgs &a, int out_dtype, cudaStream_t s)
     const uint64_t r[1] = {uint64_t(a.R)};
     const uint64_t dn[3] = {uint64_t(a.N), uint64_t(a.M), uint64_t(a.G)};
     const uint64_t rn[2] = {uint64_t(a.N) * es, uint64_t(a.N) * uint64_t(a.M) * es};
-    const uint32_t ba[2] = {BK, BM}, bb[2] = {BK, 128}, bo[3] = {uint32_t(128 / es), 32, 1};
+    const uint32_t ba[2] = {BK, BM}, bb[2] = {BK, P::BN}, bo[3] = {uint32_t(128 / es), 32, 1};
     if (!tmap_u8(&ta, a.a, 2, da, r, ba) || !tmap_u8(&tb, a.b, 2, db, r, bb) ||
         !tmap_out(&to, a.out, out_dtype, 3, dn, rn, bo))
         return cudaErrorInvalidValue;
     return by_type<P, true>(ta, tb, to, p, a.G * p.mt * p.nt, out_dtype, s);
 }
 
+// Whether tiles of 128 x 256 are done sooner, from the numbers of row tiles and
+// columns: by rounds of one tile an SM, where a narrow tile takes 0.64 of a wide
+// one's time (65536 rows of 64 experts, 4096 x 4096: 1289 us of 1007; 65536 rows of 8,
+// K 2048, 384 columns: 72 of 69; one segment of 512 rows, 2816 columns, less than a
+// round either way: 14 of 20; weights 1024 x 1024 from 8192 rows, likewise: 33 of 48;
+// 128 columns, half of a wide tile empty: 58 of 77).
+bool wide_sooner(int64_t row_tiles, int64_t N)
+{
+    const int64_t sms = num_sms();
+    const int64_t narrow = (row_tiles * ((N + 127) / 128) + sms - 1) / sms;
+    const int64_t wide = (row_tiles * ((N + 255) / 256) + sms - 1) / sms;
+    return 25 * wide <= 16 * narrow;
+}
+
 }  // namespace
 
+// Where the weights' way through HBM counts the wide tile's gain is small: with fewer
+// than 160 rows a segment it must not leave half of its last tile empty (7001 rows of
+// 61 experts, 1328 columns: narrow 138 us, wide 142; 8192 rows of 64, 2816 columns: 174
+// and 155; 4096 rows: 138 and 132), and with fewer than 64 narrow tiles, which have more
+// stages, are the faster (296 rows of 60: 121 and 124).
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs &a, int out_dtype, cudaStream_t s)
 {
-    return a.R >= 160 * a.G ? gemm_rows<Pair>(a, out_dtype, s) : gemm_rows<One>(a, out_dtype, s);
+    const bool rows = a.R >= 160 * a.G || (a.R >= 64 * a.G && (a.N + 127) / 128 % 2 == 0);
+    const bool wide = rows && wide_sooner(a.R / BM + std::min(a.G, a.R), a.N);
+    return wide ? gemm_rows<Wide>(a, out_dtype, s) : gemm_rows<Narrow>(a, out_dtype, s);
 }
 
 cudaError_t launch_fp8_wgrad(const Fp8WgradArgs &a, int out_dtype, cudaStream_t s)
 {
-    return a.M > BM ? gemm_weights<Pair>(a, out_dtype, s) : gemm_weights<One>(a, out_dtype, s);
+    return wide_sooner(a.G * ((a.M + BM - 1) / BM), a.N) ? gemm_weights<Wide>(a, out_dtype, s)
+                                                        : gemm_weights<Narrow>(a, out_dtype, s);
 }
 
 }  // namespace mhc

@@ -206,6 +206,29 @@ def test_gemm(M, counts, align, N, K, extra, fa, fb):
         check(out, ref, mag, F8.product_ops(K), str(dtype))
 
 
+@pytest.mark.parametrize("counts,align,N,K,extra", [
+    ([1500, 0, 900, 131], 1, 2824, 272, 5),      # enough tiles for the wider form, odd ends
+    ([100] * 24, 8, 1536, 144, 0),               # below 160 rows a segment, whole tiles
+    ([5000], 16, 2056, 128, 100),                # one block; more row tiles than two groups
+])
+@pytest.mark.parametrize("fa,fb", [(E4M3, E4M3), (E5M2, E4M3)])
+def test_gemm_of_many_tiles(M, counts, align, N, K, extra, fa, fb):
+    """And some of the rows in a small call of their own have the bits that they have here."""
+    a, sa, b, sb, off, R = gemm_case(counts, align, N, K, fa, fb, N + K, extra)
+    ref, mag = gemm_ref(a, sa, b, sb, off)
+    dev = [t.cuda() for t in (a, sa, b, sb, off)]
+    for dtype in DTYPES:
+        out = full(R, N, dtype=dtype)
+        M.mhc_fp8_gemm(*dev, out)
+        check(out, ref, mag, F8.product_ops(K), str(dtype))
+    hi = int(off[-1])
+    lo = hi - 90
+    few = full(90, N)
+    own = dev[1][:, lo:hi].clone(memory_format=torch.contiguous_format)
+    M.mhc_fp8_gemm(dev[0][lo:hi], own, dev[2][-1:], dev[3][-1:].clone(), None, few)
+    assert torch.equal(few, out[lo:hi])
+
+
 def test_gemm_many_experts(M):
     """As many as are allowed, most of them without a row."""
     counts = [3 if e % 7 == 0 else 0 for e in range(1024)]
@@ -264,6 +287,18 @@ def wgrad_ref(at, sat, bt, sbt, off):
     ([1, 0, 2, 129, 40], 72, 1328, 0)])
 @pytest.mark.parametrize("fa,fb", [(E4M3, E4M3), (E5M2, E4M3)])
 def test_wgrad(M, counts, M_, N, extra, fa, fb):
+    case = wgrad_case(counts, M_, N, fa, fb, M_, extra)
+    ref, mag = wgrad_ref(*case)
+    for dtype in DTYPES:
+        out = full(len(counts), M_, N, dtype=dtype)
+        M.mhc_fp8_wgrad(*(t.cuda() for t in case), out)
+        check(out, ref, mag, F8.product_ops(max(counts) + 1), str(dtype))
+
+
+@pytest.mark.parametrize("counts,M_,N,extra", [
+    ([130, 0, 300, 1], 1000, 2824, 128), ([40] * 30, 136, 1536, 0)])
+@pytest.mark.parametrize("fa,fb", [(E4M3, E4M3), (E5M2, E4M3)])
+def test_wgrad_of_many_tiles(M, counts, M_, N, extra, fa, fb):
     case = wgrad_case(counts, M_, N, fa, fb, M_, extra)
     ref, mag = wgrad_ref(*case)
     for dtype in DTYPES:
