@@ -13,8 +13,8 @@
 // in registers need no trip through shared memory.
 //
 // Work: (segment, tile) in order of the experts, a segment up to 8 slots of one
-// expert (16 at a time held twice the sums and took longer wherever it was tried,
-// 329 us for 166 with 16 slots an expert: the second 8 find the weights in L2),
+// expert (16 at a time took longer wherever it was tried, 308 us for 257 with 16
+// slots an expert: the second 8 find the weights in L2, the rows of 16 have no room in L1),
 // a tile 32 weight rows (16 of gate and the same 16 of up); a
 // block, one an SM, takes a contiguous share of it.  One to 16 warps split a
 // tile's k in pieces and join through shared memory in a fixed order (split_of).  The next
@@ -45,7 +45,8 @@ constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kRows = 32;                 // weight rows of a tile
 constexpr int TOK = 8;                    // slots of a segment: the tensor cores' columns
 constexpr int kPitch = 36;                // floats of a token's partial sums: no bank conflicts
-constexpr int kMaxSlots = kMoeFewTokens * 32;
+constexpr int kMaxSlots = kMoeFewTokens * 32, kMaxExperts = 1024;
+constexpr int kMaxSegments = kMaxExperts + kMaxSlots / TOK;
 constexpr int kPiece = 128;               // bytes of k a warp takes at once
 enum : int { kFaultExpert = 202 };
 
@@ -147,11 +148,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
 {
     constexpr bool EIGHT = sizeof(W) == 1;
     extern __shared__ __align__(16) uint8_t smem[];
-    // slots in order of their experts, the experts' first slots and first segments
+    // slots in order of their experts, the experts' first slots and first segments, the
+    // segments' experts
     uint16_t *slots = reinterpret_cast<uint16_t *>(smem);
     int *first = reinterpret_cast<int *>(smem + kMaxSlots * 2);
-    int *fseg = first + 1028;
-    float *red = reinterpret_cast<float *>(fseg + 1028);  // [2][warps][TOK][kPitch]
+    int *fseg = first + kMaxExperts + 4;
+    uint16_t *expert = reinterpret_cast<uint16_t *>(fseg + kMaxExperts + 4);
+    float *red = reinterpret_cast<float *>(expert + kMaxSegments);  // [2][warps][TOK][kPitch]
     uint8_t *xs = reinterpret_cast<uint8_t *>(red + 2 * kWarps * TOK * kPitch);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -163,7 +166,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
     // came before up is done; only h is its work.
     if (!DOWN) pdl_wait();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    int *ids = reinterpret_cast<int *>(red);  // not in use yet
+    // Every block sorts the slots by their experts, in the same order.  (A thread an expert
+    // that looks at all slots, twice: 188 us of 132 with 1024 slots of 64 experts, 2048 x 768.)
+    int *ids = reinterpret_cast<int *>(red), *count = ids + kMaxSlots;  // red is not in use yet
+    int *sums = count + kMaxExperts;
+    for (int e = tid; e < E; e += kThreads) count[e] = 0;
     for (int i = tid; i < n; i += kThreads) {
         int e = __ldg(p.ids + i);
         if (e < -1 || e >= E) {
@@ -173,41 +180,53 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
         ids[i] = e;
     }
     __syncthreads();
-    for (int e = tid; e < E; e += kThreads) {
-        int c = 0;
-        for (int i = 0; i < n; ++i) c += ids[i] == e;
-        first[e + 1] = c;
-        fseg[e + 1] = (c + TOK - 1) / TOK;
-    }
-    if (tid == 0) first[0] = fseg[0] = 0;
-    __syncthreads();
-    if (warp == 0) {
-        int a = 0, b = 0;
-        for (int e0 = 1; e0 <= E; e0 += 32) {
-            const int e = e0 + lane;
-            int u = e <= E ? first[e] : 0, v = e <= E ? fseg[e] : 0;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int ou = __shfl_up_sync(kFull, u, d), ov = __shfl_up_sync(kFull, v, d);
-                if (lane >= d) {
-                    u += ou;
-                    v += ov;
-                }
+    if (warp == 0) {  // a slot's place among its expert's, above the id's bits: 32 slots a step
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane, e = i < n ? ids[i] : -1;
+            const uint32_t same = __match_any_sync(kFull, e);
+            const int before = e >= 0 ? count[e] : 0, at = __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (e >= 0) {
+                ids[i] = e | (before + at) << 10;
+                if (at == 0) count[e] = before + __popc(same);
             }
-            if (e <= E) {
-                first[e] = u + a;
-                fseg[e] = v + b;
-            }
-            a += __shfl_sync(kFull, u, 31);
-            b += __shfl_sync(kFull, v, 31);
+            __syncwarp();
         }
     }
     __syncthreads();
-    for (int e = tid; e < E; e += kThreads) {
-        int at = first[e];
-        if (first[e + 1] > at)
-            for (int i = 0; i < n; ++i)
-                if (ids[i] == e) slots[at++] = uint16_t(i);
+    {
+        // two experts a thread; numbers of slots below, of segments above bit 16
+        static_assert(kMaxExperts == 2 * kThreads && kMaxExperts <= 1 << 10, "experts");
+        static_assert(kMaxSegments < 1 << 15 && kMaxSlots < 1 << 16, "two numbers in a word");
+        const int e = 2 * tid, c0 = e < E ? count[e] : 0, c1 = e + 1 < E ? count[e + 1] : 0;
+        const int a0 = c0 | (c0 + TOK - 1) / TOK << 16, a1 = c1 | (c1 + TOK - 1) / TOK << 16;
+        int v = a0 + a1;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(kFull, v, d);
+            if (lane >= d) v += o;
+        }
+        if (lane == 31) sums[warp] = v;
+        __syncthreads();
+        v += int(__reduce_add_sync(kFull, lane < warp ? unsigned(sums[lane]) : 0u)) - a0 - a1;
+        for (int j = 0; j < 2; ++j) {
+            if (e + j <= E) {
+                first[e + j] = v & 0xffff;
+                fseg[e + j] = v >> 16;
+            }
+            const int c = j ? a1 : a0;
+            for (int q = 0; q < c >> 16; ++q) expert[(v >> 16) + q] = uint16_t(e + j);
+            v += c;
+        }
+        if (tid == kThreads - 1 && E == kMaxExperts) {
+            first[E] = v & 0xffff;
+            fseg[E] = v >> 16;
+        }
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kThreads) {
+        const int v = ids[i];
+        if (v >= 0) slots[first[v & 1023] + (v >> 10)] = uint16_t(i);
     }
     __syncthreads();
     const int nseg = fseg[E];
@@ -229,24 +248,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
     float *sx = reinterpret_cast<float *>(xs + (EIGHT ? TOK * xpitch : 0));  // [nkb][TOK]
     const uint8_t *wt = static_cast<const uint8_t *>(p.wt);
 
-    const int64_t total = int64_t(nseg) * p.ntiles;
-    const int64_t t_begin = total * blockIdx.x / gridDim.x;
-    const int64_t t_end = total * (blockIdx.x + 1) / gridDim.x;
+    const int total = nseg * p.ntiles;  // kMaxSegments * kMoeFewMaxK / 16 at most
+    const int t_begin = int(int64_t(total) * blockIdx.x / gridDim.x);
+    const int t_end = int(int64_t(total) * (blockIdx.x + 1) / gridDim.x);
     bool waited = !DOWN;
     int parity = 0;
 
-    for (int64_t t0 = t_begin; t0 < t_end;) {
-        const int seg = int(t0 / p.ntiles);
-        const int64_t t1 = min(t_end, int64_t(seg + 1) * p.ntiles);
-        int lo = 0, hi = E;  // the last e with fseg[e] <= seg: an expert with slots
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (fseg[mid] <= seg)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const int e = lo;
+    for (int t0 = t_begin; t0 < t_end;) {
+        const int seg = t0 / p.ntiles;
+        const int t1 = min(t_end, (seg + 1) * p.ntiles);
+        const int e = expert[seg];
         const int s0 = first[e] + (seg - fseg[e]) * TOK;
         const int ns = min(TOK, first[e + 1] - s0);
         const uint8_t *we = wt + int64_t(e) * p.rows * Kb;
@@ -256,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
         };
         // this warp's pieces: wk, wk + WK, ... of tiles gi, gi + NG, ...; where the next one
         // stands is stepped, as an instruction costs a warp beside 15 others five cycles
-        const int tile0 = int(t0 - int64_t(seg) * p.ntiles), tile1 = int(t1 - int64_t(seg) * p.ntiles);
+        const int tile0 = t0 - seg * p.ntiles, tile1 = t1 - seg * p.ntiles;
         int ltile = tile0 + gi, lpiece = wk;
         const uint8_t *la[2];  // row g of the row groups, this lane's bytes of the piece
         const float *ls[2];    // the row groups' scales of the piece
@@ -499,14 +510,25 @@ __global__ void __launch_bounds__(128) k_moe_few_sum(const float *__restrict__ y
     pdl_wait();
     if (t >= T) return;
     float sum[8] = {};
-    for (int j = 0; j < k; ++j) {
-        const int slot = t * k + j, e = __ldg(ids + slot);
-        if (e < 0 || e >= E) continue;
-        const float *row = y + int64_t(slot) * C + c;
-        const float4 a = *reinterpret_cast<const float4 *>(row), b = *reinterpret_cast<const float4 *>(row + 4);
-        const float m = __ldg(w + slot), v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    constexpr int U = 8;  // slots whose loads are in flight together
+    for (int j0 = 0; j0 < k; j0 += U) {
+        float m[U], v[U][8];
+        bool in[U];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) sum[q] = fmaf(m, v[q], sum[q]);
+        for (int j = 0; j < U; ++j) {
+            in[j] = j0 + j < k;
+            if (!in[j]) continue;
+            const int slot = t * k + j0 + j, e = __ldg(ids + slot);
+            const float *row = y + int64_t(slot) * C + c;  // of a slot without an expert: not used
+            *reinterpret_cast<float4 *>(&v[j][0]) = __ldcg(reinterpret_cast<const float4 *>(row));
+            *reinterpret_cast<float4 *>(&v[j][4]) = __ldcg(reinterpret_cast<const float4 *>(row + 4));
+            m[j] = __ldg(w + slot);
+            in[j] = e >= 0 && e < E;
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) sum[q] = in[j] ? fmaf(m[j], v[j][q], sum[q]) : sum[q];
     }
     Vec<X, 8> o;
     narrow<X, 8>(sum, o);
@@ -516,7 +538,7 @@ __global__ void __launch_bounds__(128) k_moe_few_sum(const float *__restrict__ y
 size_t few_smem(bool eight, int64_t K)
 {
     const int64_t nkb = fp8_blocks(K);
-    int64_t b = kMaxSlots * 2 + 1028 * 2 * 4 + 2 * kWarps * TOK * kPitch * 4;
+    int64_t b = kMaxSlots * 2 + (kMaxExperts + 4) * 2 * 4 + kMaxSegments * 2 + 2 * kWarps * TOK * kPitch * 4;
     if (eight) b += TOK * (nkb * kFp8Block + 64) + nkb * TOK * 4;
     return size_t(b);
 }

@@ -388,6 +388,13 @@ def test_few(M, T, C, F, E, k, dtype, eight):
     F8.check_few(few_run(M, case), *few_ref(case))
 
 
+@pytest.mark.parametrize("T,E,k", [(128, 1024, 32), (128, 1023, 32), (128, 4, 4), (5, 1024, 1), (1, 33, 32)])
+@pytest.mark.parametrize("eight", [False, True])
+def test_few_most_slots_and_experts(M, T, E, k, eight):
+    case = few_case(T, 32, 16, E, k, torch.bfloat16, eight, T + E)
+    F8.check_few(few_run(M, case), *few_ref(case))
+
+
 @pytest.mark.parametrize("eight", [False, True])
 def test_few_drops_twins_and_strangers(M, eight):
     """No slot at all, an expert named twice by a token, ids outside."""
