@@ -45,9 +45,16 @@ __device__ __forceinline__ float f8_up(uint32_t amax)
     return __fdiv_rn(f8_top<FMT>(), __uint_as_float(amax));
 }
 
-// 1 / (1 + exp(-g)): 0 where exp(-g) is inf.
-__device__ __forceinline__ float sigm(float g) { return rcp_approx(1.f + __expf(-g)); }
-// g p for p = sigm(g), 0 at -inf
-__device__ __forceinline__ float silu(float g, float p) { return p == 0.f ? 0.f : g * p; }
+// 1 / (1 + exp(-g)): 0 where exp(-g) is inf.  An exp(-g) that is no normal number may be
+// zero beside 1.
+__device__ __forceinline__ float sigm(float g)
+{
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    return rcp_approx(1.f + e);
+}
+// g p for p = sigm(g), 0 at -inf; NaN comes with p
+__device__ __forceinline__ float silu_bound(float g) { return fmaxf(g, -3.4028234e38f); }
+__device__ __forceinline__ float silu(float g, float p) { return silu_bound(g) * p; }
 
 }  // namespace mhc

@@ -83,9 +83,17 @@ constexpr int kSources = SRC == kFp8Plain ? 1 : SRC == kFp8Swiglu ? 2 : 3;
 // Whether a block walks over tiles and brings the next one to shared memory while it
 // works on this one.  16384 x 4096 in fp32 took 96 us so and 74 a block a tile, the
 // activation in fp32 85 and 66, 73664 x 4096 in bf16 220 and 238, the activation in
-// bf16 168 and 214; three sources leave no room for two blocks.
+// bf16 168 and 214, its gradient (32768 x 2048) 190 and 198.
 template <class T, int SRC>
-constexpr bool kStaged = sizeof(T) == 2 && kSources<SRC> <= 2;
+constexpr bool kStaged = sizeof(T) == 2;
+
+// c = a b
+__device__ __forceinline__ void mul8(const float (&a)[8], const float (&b)[8], float (&c)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+        f2_split(f2_mul(f2_make(a[j], a[j + 1]), f2_make(b[j], b[j + 1])), c[j], c[j + 1]);
+}
 
 // The thread's row i from its 8 values of each source.
 template <class T, int SRC>
@@ -97,19 +105,31 @@ __device__ __forceinline__ void hold(Held<T, SRC> &h, int i, const Vec<T, 8> &wg
     } else if constexpr (SRC == kFp8Plain) {
         widen<T, 8>(wg, h.v[i]);
     } else {
-        float gv[8], uv[8], dv[8];
+        float gv[8], uv[8], dv[8], p[8], a[8];
         widen<T, 8>(wg, gv);
         if constexpr (SRC == kFp8SwigluGrad) widen<T, 8>(wd, dv);
-        if (up_part) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) h.v[i][j] = dv[j] * silu(gv[j], sigm(gv[j]));
+        for (int j = 0; j < 8; ++j) p[j] = sigm(gv[j]);
+        // silu(gate), then pairs: up's gradient d a, gate's d u (p + a (1 - p)), the product a u
+#pragma unroll
+        for (int j = 0; j < 8; ++j) gv[j] = silu_bound(gv[j]);
+        mul8(gv, p, a);
+        if (up_part) {
+            mul8(dv, a, h.v[i]);
             return;
         }
         widen<T, 8>(wu, uv);
+        if constexpr (SRC == kFp8Swiglu) {
+            mul8(a, uv, h.v[i]);
+        } else {
+            mul8(dv, uv, uv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float p = sigm(gv[j]), a = silu(gv[j], p);
-            h.v[i][j] = SRC == kFp8Swiglu ? a * uv[j] : dv[j] * uv[j] * (p + a * (1.f - p));
+            for (int j = 0; j < 8; j += 2) {
+                const f32x2 pp = f2_make(p[j], p[j + 1]);
+                const f32x2 q = f2_fma(pp, f2_make(-1.f, -1.f), f2_make(1.f, 1.f));
+                f2_split(f2_mul(f2_make(uv[j], uv[j + 1]), f2_fma(f2_make(a[j], a[j + 1]), q, pp)),
+                         h.v[i][j], h.v[i][j + 1]);
+            }
         }
     }
 }
@@ -149,10 +169,17 @@ template <class T, int FMT, int SRC, bool TILES>
 __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a, int halves)
 {
     typedef Held<T, SRC> H;
+    // A row's magnitude stands where its quotient comes after, the columns' magnitudes by warps
+    // where the bytes along them do: with three sources two blocks fill the SM's 228 KB, and
+    // where nothing is staged the L1 is the larger (73 -> 70 us).  Elsewhere the barrier between
+    // the tiles would cost 1%.
+    constexpr bool ALIAS = !kStaged<T, SRC> || kSources<SRC> == 3;
     __shared__ __align__(16) uint8_t tile[B * B];
-    __shared__ __align__(16) uint32_t col_part[kWarps][B];
-    __shared__ __align__(16) uint32_t row_m[B];
+    __shared__ __align__(16) uint32_t col_own[ALIAS ? 1 : kWarps][B];
+    uint32_t(*col_part)[B] = ALIAS ? reinterpret_cast<uint32_t(*)[B]>(tile) : col_own;
+    static_assert(sizeof(uint32_t) * kWarps * B <= sizeof(tile), "columns' magnitudes");
     __shared__ __align__(16) float row_up[B], col_up[B];
+    uint32_t *row_m = reinterpret_cast<uint32_t *>(row_up);
     extern __shared__ __align__(16) uint8_t next[];  // [source][row][half of it][thread] 16 bytes
     constexpr int PER = int(sizeof(T)) / 2;           // 16-byte pieces of 8 values
     constexpr bool STAGED = kStaged<T, SRC>;
@@ -173,8 +200,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
                 const uint32_t at = mine + (i * PER + k) * kThreads * 16;
                 constexpr int SLOT = kRows * PER * kThreads * 16;
                 cp_async16(at, n ? q.x + i * q.step + k * 4 : a.x, n);
-                if constexpr (SRC == kFp8Swiglu)
+                if (SRC == kFp8Swiglu || (SRC == kFp8SwigluGrad && !q.up_part))
                     cp_async16(at + SLOT, n ? q.u + i * q.step + k * 4 : a.x, n);
+                if constexpr (SRC == kFp8SwigluGrad)
+                    cp_async16(at + 2 * SLOT, n ? q.d + i * q.dstep + k * 4 : a.x, n);
             }
     };
     auto take = [&](Vec<T, 8> &w, int source, int i) {
@@ -203,7 +232,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
         Vec<T, 8> wg, wu, wd;
         if constexpr (STAGED) {
             take(wg, 0, i);
-            if constexpr (SRC == kFp8Swiglu) take(wu, 1, i);
+            if (SRC == kFp8Swiglu || (SRC == kFp8SwigluGrad && !part.up_part)) take(wu, 1, i);
+            if constexpr (SRC == kFp8SwigluGrad) take(wd, 2, i);
             hold<T, SRC>(held, i, wg, wu, wd, part.up_part);
         } else if (i < rows) {
             ld_vec<T, 8>(wg, part.x + i * part.step);
@@ -275,16 +305,18 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
 #pragma unroll
         for (int k = 0; k < 8; ++k) cm[k] = 0;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            rm[i] = 0;
+        for (int i = 0; i < kRows; ++i) rm[i] = 0;
+#pragma unroll
+        for (int i = 0; i < kRows; i += 2)
 #pragma unroll
             for (int k = 0; k < 8; k += 2) {
-                const uint32_t x = f8_mag(held.v[i][k]), y = f8_mag(held.v[i][k + 1]);
-                rm[i] = __vimax3_u32(rm[i], x, y);
-                cm[k] = max(cm[k], x);
-                cm[k + 1] = max(cm[k + 1], y);
+                const uint32_t x0 = f8_mag(held.v[i][k]), y0 = f8_mag(held.v[i][k + 1]);
+                const uint32_t x1 = f8_mag(held.v[i + 1][k]), y1 = f8_mag(held.v[i + 1][k + 1]);
+                rm[i] = __vimax3_u32(rm[i], x0, y0);
+                rm[i + 1] = __vimax3_u32(rm[i + 1], x1, y1);
+                cm[k] = __vimax3_u32(cm[k], x0, x1);
+                cm[k + 1] = __vimax3_u32(cm[k + 1], y0, y1);
             }
-        }
         if (a.q && !TILES) {
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
@@ -344,10 +376,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             if (i < rows) {
+                const float ups[8] = {up[i], up[i], up[i], up[i], up[i], up[i], up[i], up[i]};
                 float f[8];
                 held.row(i, f);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) f[k] *= up[i];
+                mul8(f, ups, f);
                 *reinterpret_cast<uint2 *>(q + i * C) =
                     make_uint2(f8_cvt4<FMT>(f[0], f[1], f[2], f[3]), f8_cvt4<FMT>(f[4], f[5], f[6], f[7]));
             }
@@ -373,8 +405,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             held.row(i, tc[i]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) tc[i][k] *= cu[k];
+            mul8(tc[i], cu, tc[i]);
         }
     }
 #pragma unroll
@@ -391,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
         if (col < C && row < R)  // R is a multiple of 16
             *reinterpret_cast<uint4 *>(a.qt + (g * C + col) * R + row) = w;
     }
+    if (STAGED && ALIAS) __syncthreads();  // the next tile's magnitudes come where these bytes were
     }
 }
 
