@@ -39,6 +39,12 @@ __device__ __forceinline__ void cp_async16(uint32_t to, const void *from, uint32
                  : "memory");
 }
 
+__device__ __forceinline__ void sts128(uint32_t to, float x, float y, float z, float w)
+{
+    asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" ::"r"(to), "f"(x), "f"(y), "f"(z), "f"(w)
+                 : "memory");
+}
+
 constexpr int kRows = 4, kThreads = B / kRows * 16, kWarps = kThreads / 32;
 // What a thread holds of the tile: 4 rows x 8 columns.
 template <class T, int SRC>
@@ -84,7 +90,7 @@ constexpr int kSources = SRC == kFp8Plain ? 1 : SRC == kFp8Swiglu ? 2 : 3;
 // works on this one.  16384 x 4096 in fp32 took 96 us so and 74 a block a tile, the
 // activation in fp32 85 and 66, 73664 x 4096 in bf16 220 and 238, the activation in
 // bf16 168 and 214, its gradient (32768 x 2048) 190 and 198.
-template <class T, int SRC>
+template <class T>
 constexpr bool kStaged = sizeof(T) == 2;
 
 // c = a b
@@ -93,6 +99,19 @@ __device__ __forceinline__ void mul8(const float (&a)[8], const float (&b)[8], f
 #pragma unroll
     for (int j = 0; j < 8; j += 2)
         f2_split(f2_mul(f2_make(a[j], a[j + 1]), f2_make(b[j], b[j + 1])), c[j], c[j + 1]);
+}
+
+// c = du (p + a (1 - p))
+__device__ __forceinline__ void gate_grad(const float (&du)[8], const float (&a)[8],
+                                          const float (&p)[8], float (&c)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        const f32x2 pp = f2_make(p[j], p[j + 1]);
+        const f32x2 q = f2_fma(pp, f2_make(-1.f, -1.f), f2_make(1.f, 1.f));
+        f2_split(f2_mul(f2_make(du[j], du[j + 1]), f2_fma(f2_make(a[j], a[j + 1]), q, pp)), c[j],
+                 c[j + 1]);
+    }
 }
 
 // The thread's row i from its 8 values of each source.
@@ -123,15 +142,29 @@ __device__ __forceinline__ void hold(Held<T, SRC> &h, int i, const Vec<T, 8> &wg
             mul8(a, uv, h.v[i]);
         } else {
             mul8(dv, uv, uv);
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-                const f32x2 pp = f2_make(p[j], p[j + 1]);
-                const f32x2 q = f2_fma(pp, f2_make(-1.f, -1.f), f2_make(1.f, 1.f));
-                f2_split(f2_mul(f2_make(uv[j], uv[j + 1]), f2_fma(f2_make(a[j], a[j + 1]), q, pp)),
-                         h.v[i][j], h.v[i][j + 1]);
-            }
+            gate_grad(uv, a, p, h.v[i]);
         }
     }
+}
+
+// Row i of the gate's gradient, and of up's beside it.
+template <class T>
+__device__ __forceinline__ void hold_both(Held<T, kFp8SwigluGrad> &h, float (&up)[8], int i,
+                                          const Vec<T, 8> &wg, const Vec<T, 8> &wu,
+                                          const Vec<T, 8> &wd)
+{
+    float gv[8], uv[8], dv[8], p[8];
+    widen<T, 8>(wg, gv);
+    widen<T, 8>(wu, uv);
+    widen<T, 8>(wd, dv);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) p[j] = sigm(gv[j]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) gv[j] = silu_bound(gv[j]);
+    mul8(gv, p, gv);
+    mul8(dv, gv, up);
+    mul8(dv, uv, uv);
+    gate_grad(uv, gv, p, h.v[i]);
 }
 
 // A thread's part of a tile: where it stands.
@@ -165,7 +198,11 @@ struct Part {
     }
 };
 
-template <class T, int FMT, int SRC, bool TILES>
+// PAIRS: the gate's tile and the up tile of the same columns one after the other, from one
+// reading and one sigm; up's values wait in the thread's staging places, in fp32.  Where the
+// blocks of 128 end with the gate's columns (32768 x 2048: 134 us, one by one 169; along the
+// rows alone 104 and 143); elsewhere up's blocks begin inside the gate's.
+template <class T, int FMT, int SRC, bool TILES, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a, int halves)
 {
     typedef Held<T, SRC> H;
@@ -173,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
     // where the bytes along them do: with three sources two blocks fill the SM's 228 KB, and
     // where nothing is staged the L1 is the larger (73 -> 70 us).  Elsewhere the barrier between
     // the tiles would cost 1%.
-    constexpr bool ALIAS = !kStaged<T, SRC> || kSources<SRC> == 3;
+    constexpr bool ALIAS = !kStaged<T> || kSources<SRC> == 3;
     __shared__ __align__(16) uint8_t tile[B * B];
     __shared__ __align__(16) uint32_t col_own[ALIAS ? 1 : kWarps][B];
     uint32_t(*col_part)[B] = ALIAS ? reinterpret_cast<uint32_t(*)[B]>(tile) : col_own;
@@ -182,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
     uint32_t *row_m = reinterpret_cast<uint32_t *>(row_up);
     extern __shared__ __align__(16) uint8_t next[];  // [source][row][half of it][thread] 16 bytes
     constexpr int PER = int(sizeof(T)) / 2;           // 16-byte pieces of 8 values
-    constexpr bool STAGED = kStaged<T, SRC>;
+    constexpr bool STAGED = kStaged<T>;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tx = tid & 15, ty = tid >> 4;
     const int64_t R = a.R, C = a.C;
@@ -218,10 +255,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
     };
 
     pdl_wait();
-    Part<T, SRC> coming(a, halves, blockIdx.x);
+    uint32_t t = PAIRS ? 2 * blockIdx.x : blockIdx.x, next_t;
+    Part<T, SRC> coming(a, halves, t);
     if constexpr (STAGED) bring(coming);
+    for (; t < tiles; t = next_t) {
+    const bool second = PAIRS && t % 2;
     // (a block a tile where nothing is staged)
-    for (uint32_t t = blockIdx.x; t < tiles; t = STAGED ? t + gridDim.x : tiles) {
+    next_t = !STAGED ? tiles : !PAIRS ? t + gridDim.x : second ? t - 1 + 2 * gridDim.x : t + 1;
     const Part<T, SRC> part = coming;
     const int cb = part.cb, rows = part.rows;
     const int64_t rb = part.rb, g = part.g, r0 = part.r0, c0 = part.c0;
@@ -230,7 +270,23 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         Vec<T, 8> wg, wu, wd;
-        if constexpr (STAGED) {
+        if constexpr (PAIRS) {
+            const uint32_t lo = mine + i * kThreads * 16, hi = lo + kRows * kThreads * 16;
+            if (second) {
+                const uint4 v = lds128(lo), w = lds128(hi);
+                const uint32_t b[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j) held.v[i][j] = __uint_as_float(b[j]);
+            } else {
+                take(wg, 0, i);
+                take(wu, 1, i);
+                take(wd, 2, i);
+                float up[8];
+                hold_both(held, up, i, wg, wu, wd);
+                sts128(lo, up[0], up[1], up[2], up[3]);
+                sts128(hi, up[4], up[5], up[6], up[7]);
+            }
+        } else if constexpr (STAGED) {
             take(wg, 0, i);
             if (SRC == kFp8Swiglu || (SRC == kFp8SwigluGrad && !part.up_part)) take(wu, 1, i);
             if constexpr (SRC == kFp8SwigluGrad) take(wd, 2, i);
@@ -245,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
         }
     }
     if constexpr (STAGED)
-        if (t + gridDim.x < tiles) {
-            coming = Part<T, SRC>(a, halves, t + gridDim.x);
-            bring(coming);
+        if (next_t < tiles) {
+            coming = Part<T, SRC>(a, halves, next_t);
+            if (!PAIRS || second) bring(coming);
         }
     if (a.y) {
         T *y = static_cast<T *>(a.y) + (g * R + r0) * C + c0;
@@ -426,19 +482,19 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const Fp8QuantArgs a,
     }
 }
 
-template <class T, int FMT, int SRC, bool TILES>
+template <class T, int FMT, int SRC, bool TILES, bool PAIRS>
 cudaError_t run(const Fp8QuantArgs &a, const char *name, cudaStream_t s)
 {
-    auto *kernel = k_fp8_quant<T, FMT, SRC, TILES>;
-    const int smem = kStaged<T, SRC> ? kSources<SRC> * kRows * int(sizeof(T)) * 8 * kThreads : 0;
+    auto *kernel = k_fp8_quant<T, FMT, SRC, TILES, PAIRS>;
+    const int smem = kStaged<T> ? kSources<SRC> * kRows * int(sizeof(T)) * 8 * kThreads : 0;
     if (smem) {
         cudaError_t e = set_smem_limit(reinterpret_cast<const void *>(kernel), smem);
         if (e != cudaSuccess) return e;
     }
     const int halves = SRC == kFp8SwigluGrad && a.F % B == 0 ? int(a.F / B) : 0;
     // two blocks an SM that walk over the tiles, or a block a tile
-    int64_t blocks = a.G * a.nrb * a.ncb;
-    if (kStaged<T, SRC>) blocks = std::min<int64_t>(blocks, 2 * num_sms());
+    int64_t blocks = a.G * a.nrb * a.ncb / (PAIRS ? 2 : 1);
+    if (kStaged<T>) blocks = std::min<int64_t>(blocks, 2 * num_sms());
     MHC_PROF(name, s);
     return launch_k(kernel, dim3(unsigned(blocks)), dim3(kThreads), smem, s,
                     a, halves);
@@ -447,10 +503,15 @@ cudaError_t run(const Fp8QuantArgs &a, const char *name, cudaStream_t s)
 template <class T, int FMT>
 cudaError_t by_source(const Fp8QuantArgs &a, int source, cudaStream_t s)
 {
-    if (source == kFp8Swiglu) return run<T, FMT, kFp8Swiglu, false>(a, "k_fp8_swiglu_fwd", s);
-    if (source == kFp8SwigluGrad) return run<T, FMT, kFp8SwigluGrad, false>(a, "k_fp8_swiglu_bwd", s);
-    return a.tiles ? run<T, FMT, kFp8Plain, true>(a, "k_fp8_quant", s)
-                   : run<T, FMT, kFp8Plain, false>(a, "k_fp8_quant", s);
+    if (source == kFp8Swiglu) return run<T, FMT, kFp8Swiglu, false, false>(a, "k_fp8_swiglu_fwd", s);
+    if (source == kFp8SwigluGrad) {
+        if constexpr (kStaged<T>)
+            if (a.F % B == 0)
+                return run<T, FMT, kFp8SwigluGrad, false, true>(a, "k_fp8_swiglu_bwd", s);
+        return run<T, FMT, kFp8SwigluGrad, false, false>(a, "k_fp8_swiglu_bwd", s);
+    }
+    return a.tiles ? run<T, FMT, kFp8Plain, true, false>(a, "k_fp8_quant", s)
+                   : run<T, FMT, kFp8Plain, false, false>(a, "k_fp8_quant", s);
 }
 
 template <class T>

@@ -138,6 +138,33 @@ def test_swiglu(M, R, F, dtype, fmt):
         assert torch.equal(only, y)
 
 
+@pytest.mark.parametrize("F", [1024, 1040])
+@pytest.mark.parametrize("which", ["q", "t", "qt"])
+def test_of_more_tiles_than_run_at_a_time(M, F, which):
+    """A block goes through several tiles, the gate's and up's of them in pairs or one by one."""
+    R = 5008
+    h, da = rows(R, 2 * F, F, torch.bfloat16), rows(R, F, F + 1, torch.bfloat16)
+    q, s, qt, st = outputs(0, R, 2 * F, E4M3, False, which)
+    M.mhc_fp8_quant(h.cuda(), q, s, qt, st)
+    for got, ref in ((q, s), F8.quant_rows(h.float(), E4M3)), ((qt, st), F8.quant_rows(h.float().t(), E4M3)):
+        if got[0] is not None:
+            assert torch.equal(bits(got[0]), bits(ref[0])) and torch.equal(bits(got[1]), bits(ref[1]))
+    for way, ref, err in ("fwd", *F8.swiglu(np64(h))), ("bwd", *F8.swiglu_grad(np64(da), np64(h))):
+        C = ref.shape[1]
+        for y in (None, full(R, C, dtype=torch.bfloat16)):
+            q, s, qt, st = outputs(0, R, C, E4M3, False, which)
+            if way == "fwd":
+                M.mhc_fp8_swiglu_fwd(h.cuda(), y, q, s, qt, st)
+            else:
+                M.mhc_fp8_swiglu_bwd(da.cuda(), h.cuda(), y, q, s, qt, st)
+            if y is not None:
+                check(y, ref, err / U, 1.0, way)
+            if q is not None:
+                F8.check_quantised(q, s, ref, err, way + " rows")
+            if qt is not None:
+                F8.check_quantised(qt, st, ref.T.copy(), err.T.copy(), way + " columns")
+
+
 def test_swiglu_gradient_against_differences(M):
     R, F, d = 16, 32, 2.0 ** -7
     h, da = rows(R, 2 * F, 1), rows(R, F, 2)
