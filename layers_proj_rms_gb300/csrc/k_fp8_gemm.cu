@@ -15,14 +15,15 @@
 // rounded to nearest, once a block.
 //
 // What bounds it: an MMA of 128 x 256 x 32 reads 12 KB of shared memory and its
-// TMA loads write as much; a block of 128 takes 855 cycles, of 512 for the products,
-// and with every SM at work the GPU is at its power limit besides.  Tiles of 128 x 256
-// move 1.5 times the products per byte of 128 x 128 (65536 rows of 64 experts, K 4096,
-// 4096 columns: 1007-1081 us of 1289-1330) and are taken where enough of them fill the
-// SMs; the rule and its measurements stand at wide_sooner().  Two CTAs that share a
-// tile of 256 x 256, each with half of B (cta_group::2, 32 KB in and out for the same
-// products), were 1086 us of 1081, 955 of 925 for weights: the waits across the pair
-// take what the feed gains, so there are no pairs.
+// TMA loads write as much, 855 cycles a block of 128 where the products are 512; the
+// epilogue's instructions run beside that (in pairs of fp32: 968 us of 1008, for
+// weights 777 of 930), and with every SM at work the GPU is at its power limit.  Tiles
+// of 128 x 256 move 1.5 times the products per byte of 128 x 128 (65536 rows of 64
+// experts, K 4096, 4096 columns: 968 us of 1221) and are taken where enough of them
+// fill the SMs; the rule and its measurements stand at wide_sooner().  Two CTAs that
+// share a tile of 256 x 256, each with half of B (cta_group::2, 32 KB in and out for
+// the same products), were 1037 us of 978, 787 of 783 for weights: the waits across
+// the pair take more than the feed gains, so there are no pairs.
 //
 // A CTA is persistent, one an SM: a warp that brings the operands (TMA), two that
 // issue the MMAs of the even and the odd blocks, one that brings the scales
@@ -163,13 +164,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16])
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
                  : "r"(taddr));
 }
-// 16 TMEM lanes x 32 columns as fragments: v[4 j + 2 i + c] is lane 8 i + lane / 4,
+// 16 TMEM lanes x 16 columns as fragments: v[4 j + 2 i + c] is lane 8 i + lane / 4,
 // column 8 j + 2 (lane % 4) + c.
-__device__ __forceinline__ void tmem_ld16x32(uint32_t taddr, float (&v)[16])
+__device__ __forceinline__ void tmem_ld16x16(uint32_t taddr, float (&v)[8])
 {
-    asm volatile("tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
                  : "r"(taddr));
+}
+// a += v s, for pairs
+__device__ __forceinline__ void fma_pair(float *a, f32x2 v, f32x2 s)
+{
+    f2_split(f2_fma(v, s, f2_make(a[0], a[1])), a[0], a[1]);
 }
 __device__ __forceinline__ void tmem_wait(float &through)
 {
@@ -544,8 +550,8 @@ __global__ void __launch_bounds__(P::THREADS, 1)
         int b = 0;
         for (int t = t0; t < ntiles; t += tstep) {
             const Tile x = tile_of<P, W>(p, seg, first, t);
-            // rows: acc[c], row q*32 + lane, column c;  weights: acc[16 n + v], fragment v
-            // (tmem_ld16x32) of rows 16 (n % 2), columns 32 (n / 2)
+            // rows: acc[c], row q*32 + lane, column c;  weights: acc[8 n + v], fragment v
+            // (tmem_ld16x16) of rows 16 (n % 2), columns 16 (n / 2)
             float acc[P::COLS];
 #pragma unroll
             for (int j = 0; j < P::COLS; ++j) acc[j] = 0.f;
@@ -555,7 +561,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
                 const uint32_t sc = sc0 + slot;
                 slot = slot == (P::SC - 1) * P::SC_FLOATS * 4 ? 0 : slot + P::SC_FLOATS * 4;
                 float r[4];
-                float d[16];
+                float d[W ? 8 : 16];
                 if constexpr (!W) tmem_ld16(trow + b * P::BN, d);
                 if (W) {
 #pragma unroll
@@ -571,30 +577,28 @@ __global__ void __launch_bounds__(P::THREADS, 1)
                     bar_arrive(bar_read(b), 32 * (P::EPI_WARPS + 1));
                 };
                 if constexpr (W) {
-                    constexpr int NL = P::COLS / 16;  // loads of 16 lanes x 32 columns
-                    float c[8];
+                    constexpr int NL = P::COLS / 8;  // loads of 16 lanes x 16 columns
+                    f32x2 c[2];
 #pragma unroll
                     for (int n = 0; n < NL; ++n) {
                         if (n % 2 == 0) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
+                            for (int j = 0; j < 2; ++j) {
                                 const uint2 u = lds64(
-                                    sc + (BM + h * P::COLS + (n / 2) * 32 + 8 * j + 2 * tig) * 4);
-                                c[2 * j] = __uint_as_float(u.x);
-                                c[2 * j + 1] = __uint_as_float(u.y);
+                                    sc + (BM + h * P::COLS + (n / 2) * 16 + 8 * j + 2 * tig) * 4);
+                                c[j] = f2_make(__uint_as_float(u.x), __uint_as_float(u.y));
                             }
                         }
                         float &r0 = r[2 * (n & 1)], &r1 = r[2 * (n & 1) + 1];
-                        tmem_ld16x32(d0 + (n / 2) * 32 + (uint32_t(n & 1) << 20), d);
+                        tmem_ld16x16(d0 + (n / 2) * 16 + (uint32_t(n & 1) << 20), d);
                         tmem_wait(r0, r1);
                         if (n + 1 == NL) release();
-                        float *ac = acc + 16 * n;
+                        float *ac = acc + 8 * n;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            ac[4 * j] = fmaf(d[4 * j], c[2 * j] * r0, ac[4 * j]);
-                            ac[4 * j + 1] = fmaf(d[4 * j + 1], c[2 * j + 1] * r0, ac[4 * j + 1]);
-                            ac[4 * j + 2] = fmaf(d[4 * j + 2], c[2 * j] * r1, ac[4 * j + 2]);
-                            ac[4 * j + 3] = fmaf(d[4 * j + 3], c[2 * j + 1] * r1, ac[4 * j + 3]);
+                        for (int j = 0; j < 2; ++j) {
+                            fma_pair(ac + 4 * j, f2_mul(f2_make(d[4 * j], d[4 * j + 1]), f2_make(r0, r0)), c[j]);
+                            fma_pair(ac + 4 * j + 2, f2_mul(f2_make(d[4 * j + 2], d[4 * j + 3]), f2_make(r1, r1)),
+                                     c[j]);
                         }
                     }
                 } else {
@@ -604,7 +608,8 @@ __global__ void __launch_bounds__(P::THREADS, 1)
                         tmem_wait(r[0]);
                         if (c + 1 == P::COLS / 16) release();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) acc[c * 16 + j] = fmaf(d[j], r[0], acc[c * 16 + j]);
+                        for (int j = 0; j < 16; j += 2)
+                            fma_pair(acc + c * 16 + j, f2_make(d[j], d[j + 1]), f2_make(r[0], r[0]));
                     }
                 }
             }
@@ -640,7 +645,7 @@ __global__ void __launch_bounds__(P::THREADS, 1)
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 const int cc = c * CH + 8 * jj;  // columns cc + 2 tig, + 1
-                                const float *v = acc + 16 * (2 * (cc / 32) + hi) + 4 * (cc % 32 / 8) + 2 * k;
+                                const float *v = acc + 8 * (2 * (cc / 16) + hi) + 4 * (cc % 16 / 8) + 2 * k;
                                 const int row = 16 * hi + 8 * k + g;
                                 const int byte = (8 * jj + 2 * tig) * int(sizeof(O));
                                 const uint32_t to = box + row * 128 + (((byte >> 4) ^ g) << 4) + (byte & 15);
@@ -791,10 +796,11 @@ cudaError_t gemm_weights(const Fp8WgradArgs &a, int out_dtype, cudaStream_t s)
 
 // Whether tiles of 128 x 256 are done sooner, from the numbers of row tiles and
 // columns: by rounds of one tile an SM, where a narrow tile takes 0.64 of a wide
-// one's time (65536 rows of 64 experts, 4096 x 4096: 1289 us of 1007; 65536 rows of 8,
-// K 2048, 384 columns: 72 of 69; one segment of 512 rows, 2816 columns, less than a
-// round either way: 14 of 20; weights 1024 x 1024 from 8192 rows, likewise: 33 of 48;
-// 128 columns, half of a wide tile empty: 58 of 77).
+// one's time (65536 rows of 64 experts, 4096 x 4096: 1221 us of 968; 65536 rows of 8,
+// K 2048, 384 columns: 70 of 69; one segment of 512 rows, 2816 columns, less than a
+// round either way: 14 of 20; weights 1024 x 1024 from 8192 rows, likewise: 27 of 38;
+// 61 experts' weights 1000 x 1328: 39.5 of 34.3; 128 columns, half of a wide tile
+// empty: 58 of 76).
 bool wide_sooner(int64_t row_tiles, int64_t N)
 {
     const int64_t sms = num_sms();
@@ -807,9 +813,9 @@ bool wide_sooner(int64_t row_tiles, int64_t N)
 
 // Where the weights' way through HBM counts the wide tile's gain is small: with fewer
 // than 160 rows a segment it must not leave half of its last tile empty (7001 rows of
-// 61 experts, 1328 columns: narrow 138 us, wide 142; 8192 rows of 64, 2816 columns: 174
-// and 155; 4096 rows: 138 and 132), and with fewer than 64 narrow tiles, which have more
-// stages, are the faster (296 rows of 60: 121 and 124).
+// 61 experts, 1328 columns: narrow 134 us, wide 138; 8192 rows of 64, 2816 columns: 168
+// and 152; 4096 rows: 136 and 131), and with fewer than 64 narrow tiles, which have more
+// stages, are the faster (296 rows of 60: 119 and 121.5).
 cudaError_t launch_fp8_gemm(const Fp8GemmArgs &a, int out_dtype, cudaStream_t s)
 {
     const bool rows = a.R >= 160 * a.G || (a.R >= 64 * a.G && (a.N + 127) / 128 % 2 == 0);

@@ -248,7 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
     float *sx = reinterpret_cast<float *>(xs + (EIGHT ? TOK * xpitch : 0));  // [nkb][TOK]
     const uint8_t *wt = static_cast<const uint8_t *>(p.wt);
 
-    const int total = nseg * p.ntiles;  // kMaxSegments * kMoeFewMaxK / 16 at most
+    static_assert(kMaxSegments * (kMoeFewMaxK / 16) < 1 << 30, "tiles");
+    const int total = nseg * p.ntiles;
     const int t_begin = int(int64_t(total) * blockIdx.x / gridDim.x);
     const int t_end = int(int64_t(total) * (blockIdx.x + 1) / gridDim.x);
     bool waited = !DOWN;
