@@ -604,7 +604,8 @@ MHC_API mhc_status mhc_fp8_swiglu_bwd(const void *da, const void *h, mhc_dtype d
  * e; rows of no segment are zeroed and not read.  a [R, K] with sa [blocks of
  * K, R]; b [G, N, K] with sb [G, blocks of K, blocks of N].  The gradient of
  * the rows is the same product with the transposed weights (qt, st of tiles).
- * N a multiple of 8, K of 16, G <= MHC_MOE_MAX_EXPERTS. */
+ * N a multiple of 8, K of 16, G <= MHC_MOE_MAX_EXPERTS, R <= 2^31 - 128.  A row's
+ * result does not depend on the other rows or on R. */
 MHC_API mhc_status mhc_fp8_gemm(const uint8_t *a, mhc_fp8 format_a, const float *sa,
                                 const uint8_t *b, mhc_fp8 format_b, const float *sb,
                                 const int32_t *offsets, int64_t G, int64_t R, int64_t N, int64_t K,
@@ -614,7 +615,8 @@ MHC_API mhc_status mhc_fp8_gemm(const uint8_t *a, mhc_fp8 format_a, const float 
  * at[m][r] bt[n][r], zero for an empty segment.  at [M, R] with sat [blocks
  * of R, M], bt [N, R] with sbt [blocks of R, N] (qt, st of the rows' two
  * matrices).  Segments start at multiples of 128 (sort with align 128; others
- * are rounded down and set device error 206).  N a multiple of 8, R of 16. */
+ * are rounded down and set device error 206).  N a multiple of 8, R of 16,
+ * R <= 2^31 - 128. */
 MHC_API mhc_status mhc_fp8_wgrad(const uint8_t *at, mhc_fp8 format_a, const float *sat,
                                  const uint8_t *bt, mhc_fp8 format_b, const float *sbt,
                                  const int32_t *offsets, int64_t G, int64_t R, int64_t M,

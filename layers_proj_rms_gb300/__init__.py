@@ -13,8 +13,10 @@ alpha3 [3] fp32, b [O] fp32, H_pre/H_post [T, n] fp32, H_res [T, n, n] fp32,
 u_save [T, O] fp32, r_save [T] fp32, with O = n*n + 2*n.  The operators at
 the edges of the sub-layers (mhc_qk_norm_rope_*, mhc_moe_*) take bf16, fp16 or
 fp32 activations, fp32 gammas, tables and router weights, int32 indices; q, k
-[T, H, D] may be views with any token and head strides.  Outputs are passed in
-preallocated; the library writes every element.
+[T, H, D] may be views with any token and head strides.  The experts' products
+(mhc_fp8_*, mhc_moe_few_fwd) take float8_e4m3fn and float8_e5m2 matrices with
+fp32 scales for blocks of 128.  Outputs are passed in preallocated; the library
+writes every element.
 """
 from __future__ import annotations
 

@@ -61,8 +61,8 @@ def _build_marshal(force: bool) -> None:
         return
     headers = sysconfig.get_paths()["include"]
     if not os.path.exists(os.path.join(headers, "Python.h")):
-        warnings.warn(f"no Python.h in {headers}: mhc_qk_norm_rope_* and mhc_moe_* cannot be "
-                      "called from Python (their binding, csrc/marshal.c, is not built)")
+        warnings.warn(f"no Python.h in {headers}: mhc_qk_norm_rope_*, mhc_moe_* and mhc_fp8_* cannot "
+                      "be called from Python (their binding, csrc/marshal.c, is not built)")
         return
     tmp = MARSHAL + f".tmp{os.getpid()}"
     cmd = [shutil.which("gcc") or "cc", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",

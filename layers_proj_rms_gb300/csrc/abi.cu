@@ -1184,7 +1184,8 @@ void group_args(Check &ck, int fa, int fb, const int32_t *offsets, int64_t G, in
 {
     format_ok(ck, fa, "format_a");
     format_ok(ck, fb, "format_b");
-    ck.dtype(out_dtype).range(G, 1, MHC_MOE_MAX_EXPERTS, "G").range(R, 0, INT32_MAX, "R");
+    // (the kernels count a tile of 128 past the last row in 32 bits)
+    ck.dtype(out_dtype).range(G, 1, MHC_MOE_MAX_EXPERTS, "G").range(R, 0, INT32_MAX - 127, "R");
     if (ck.st == MHC_OK && !offsets && G != 1)
         ck.st = fail(MHC_ERR_NULL_PTR, "%s: offsets is NULL and G = %lld", ck.fn, (long long)G);
     if (ck.st == MHC_OK && reinterpret_cast<uintptr_t>(offsets) % 4)

@@ -104,6 +104,14 @@ def test_wgrad_refuses(L, kw, status):
     assert L.mhc_last_error()
 
 
+@pytest.mark.parametrize("R", [(1 << 31) - 127, (1 << 31) - 112, (1 << 31) - 16, (1 << 31) - 1])
+def test_products_refuse_rows_that_tiles_count_past_32_bits(L, R):
+    assert gemm(L, R=R, N=8, K=16, G=1) == 2
+    assert wgrad(L, R=(1 << 31) - 16, M=8, N=8, G=1) == 2
+    for f in gemm, wgrad:
+        assert f(L, R=(1 << 31) - 128, N=8, G=1) in (7, 8)
+
+
 def few(L, x=A, dt=0, ids=A, w=A, w1=A, s1=None, w2=A, s2=None, T=4, k=2, E=8, C=64, F=32, f=A, ws=A,
         nb=1 << 20):
     return L.mhc_moe_few_fwd(x, dt, ids, w, w1, s1, w2, s2, T, k, E, C, F, f, ws, nb, None)
