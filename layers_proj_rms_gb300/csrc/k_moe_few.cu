@@ -548,8 +548,11 @@ size_t few_smem(bool eight, int64_t K)
 // sooner but join more often, which costs a warp about two pieces' time; fewer
 // leave warps without a tile where a block has few.  So the least of tiles in
 // turn x (pieces of a warp + 2), for as many segments as the slots can make; but
-// four at least, whose pieces are 512 bytes in a row (13 tokens, 4096 x 1408, 60
-// experts, 16 bits: 315 us with one, 269 with two, 226 with four, 219 with eight).
+// four at least, whose pieces are 512 bytes in a row.  With one, two, four, eight and 16:
+// 13 tokens, 60 experts, 4096 x 1408, 16 bits: 249, 209, 190, 183, 195 us (four are taken);
+// one token, 64 experts, 7168 x 2048, 8 bits: 82, 68, 68, 70, 75 (four); 64 tokens, 8
+// experts, 4096 x 14336, 16 bits: 809, 785, 791, 816, 872 (four); one token, 8 experts,
+// 1024 x 512, 8 bits: 14.2, 11.8, 10.4, 9.9, 10.1 (eight up, four down).
 int split_of(int64_t K, int bytes, int64_t tiles)
 {
     const int64_t np = (K * bytes + kPiece - 1) / kPiece;
