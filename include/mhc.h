@@ -633,7 +633,8 @@ MHC_API mhc_status mhc_fp8_wgrad(const uint8_t *at, mhc_fp8 format_a, const floa
  * Wu], w2 [E, C, F]: of `dtype` (s1, s2 NULL), or e4m3 with scales by tiles,
  * s1 [E, blocks of C, blocks of 2F], s2 [E, blocks of F, blocks of C]; then x
  * and the activation are quantised to e4m3 by blocks of 128 as mhc_fp8_quant
- * does, the latter from its fp32 values.  Each slot's sums are fp32 throughout.
+ * does, the latter from its fp32 values.  Each slot's sums are fp32 throughout,
+ * in an order that C, F, T k and E set: the other tokens' values do not matter.
  * T <= 128, k <= 32, C and F multiples of 16 and <= 16384.
  * ws: mhc_workspace_bytes(MHC_OP_MOE_FEW_FWD, T, k, C + F). */
 MHC_API mhc_status mhc_moe_few_fwd(const void *x, mhc_dtype dtype, const int32_t *ids,

@@ -615,3 +615,77 @@ def test_few_captured_and_back_to_back(M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(oa, fa) and torch.equal(ob, fb)
+
+
+# ---- offsets past 32 bits, calls side by side --------------------------------
+
+def random_e4m3(*shape):
+    """Finite values of every sign and exponent, made on the device."""
+    v = torch.empty(*shape, dtype=torch.uint8, device="cuda").random_(0, 0x7e)
+    return v.view(E4M3)
+
+
+def test_weights_past_32_bits(M):
+    """The last of the experts stands past 2^32 bytes; it gives what it gives as the last of three
+    (the few tokens' sums go by the number of slots and experts, so as many segments either way:
+    min(experts, slots) = 3)."""
+    E, F, C = 40, 4096, 16384
+    w1, w2 = random_e4m3(E, 2 * F, C), random_e4m3(E, C, F)
+    s1 = torch.rand(E, blocks(C), blocks(2 * F), device="cuda") * C ** -0.5
+    s2 = torch.rand(E, blocks(F), blocks(C), device="cuda") * F ** -0.5
+    x = rows(3, C, 1, torch.bfloat16).cuda() * 2.0 ** -6
+    last = [t[-3:].clone() for t in (w1, s1, w2, s2)]
+    ids = torch.full((3, 1), E - 1, dtype=I32, device="cuda")
+    w = torch.ones(3, 1, device="cuda")
+    out, one = full(3, C, dtype=torch.bfloat16), full(3, C, dtype=torch.bfloat16)
+    ws = M.workspace(M.OP_MOE_FEW_FWD, 3, 1, C + F)
+    M.mhc_moe_few_fwd(x, ids, w, w1, w2, out, ws, s1, s2)
+    M.mhc_moe_few_fwd(x, torch.full_like(ids, 2), w, last[0], last[2], one, ws, last[1], last[3])
+    assert torch.equal(out, one) and out.float().abs().max() > 0 and out.isfinite().all()
+    xq, xs = full(3, C, dtype=E4M3), full(blocks(C), 3)
+    M.mhc_fp8_quant(x, xq, xs)
+    off = torch.tensor([0] * E + [3], dtype=I32, device="cuda")
+    h, alone = full(3, 2 * F), full(3, 2 * F)
+    M.mhc_fp8_gemm(xq, xs, w1, s1, off, h)
+    M.mhc_fp8_gemm(xq, xs, last[0][2:], last[1][2:].clone(), None, alone)
+    assert torch.equal(h, alone) and h.abs().max() > 0 and h.isfinite().all()
+
+
+def test_rows_past_32_bits(M):
+    """Quantised along both; the last rows and columns of 2^32 elements and more."""
+    R, C = 262272, 16400
+    x = torch.empty(R, C, dtype=torch.bfloat16, device="cuda").normal_()
+    q, s, qt, st = outputs(0, R, C, E4M3, False, "qt")
+    M.mhc_fp8_quant(x, q, s, qt, st)
+    tail = x[-128:].clone()
+    tq, ts, tqt, tst = outputs(0, 128, C, E4M3, False, "qt")
+    M.mhc_fp8_quant(tail, tq, ts, tqt, tst)
+    assert torch.equal(bits(q[-128:]), bits(tq)) and torch.equal(s[:, -128:], ts)
+    assert torch.equal(bits(qt[:, -128:]), bits(tqt)) and torch.equal(st[-1:], tst)
+
+
+def test_calls_side_by_side(M):
+    """Two streams, each with its own layer, products and workspace."""
+    cases = [few_case(T, 272, 144, 12, 3, torch.bfloat16, eight, T) for T, eight in ((20, True), (64, False))]
+    want = [few_run(M, c) for c in cases]
+    gemms = [gemm_case([700, 130], 8, 1040, 400, E4M3, E4M3, n) for n in (5, 6)]
+    gemms = [[t.cuda() for t in g[:5]] + [g[5]] for g in gemms]
+    outs = [full(g[5], 1040) for g in gemms]
+    for g, o in zip(gemms, outs):
+        M.mhc_fp8_gemm(*g[:5], o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    dev = [[None if t is None else t.cuda() for t in c] for c in cases]
+    ws = [M.workspace(M.OP_MOE_FEW_FWD, c[0].shape[0], 3, 272 + 144) for c in cases]
+    got = [[full(*w.shape, dtype=w.dtype) for _ in range(8)] for w in want]
+    prod = [[torch.empty_like(o) for _ in range(8)] for o in outs]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for n, st in enumerate(streams):
+            x, ids, w, w1, s1, w2, s2 = dev[n]
+            M.mhc_moe_few_fwd(x, ids, w, w1, w2, got[n][k], ws[n], s1, s2, stream=st)
+            M.mhc_fp8_gemm(*gemms[n][:5], prod[n][k], stream=st)
+    torch.cuda.synchronize()
+    for n in range(2):
+        assert all(torch.equal(g, want[n]) for g in got[n])
+        assert all(torch.equal(p, outs[n]) for p in prod[n])
