@@ -20,10 +20,14 @@
 // tile's k in pieces and join through shared memory in a fixed order (split_of).  The next
 // piece is always in flight: 16 warps x 4 KB an SM.
 //
-// 16-bit weights: x as it is; h as two terms of the type (its rounding and the
-// rest), so nothing is lost between the products.  8-bit weights: x and h are
-// quantised by blocks of 128, as mhc_fp8_quant does, when a segment's rows are
-// brought to shared memory; each block's product is scaled into fp32 sums.
+// h stands in the workspace in fp32.  16-bit weights: x as it is; h is split where it is
+// read into terms of the type: three of bf16, which hold all of its 24 bits, or, of
+// fp16, two of the values times a power of two that brings the largest of the 32 that a
+// column has in a step to [2^14, 2^15), undone in the fp32 sums: off by 2^-23 of the
+// value or 2^-40 of that largest (unscaled terms overflow at 65504 and are
+// subnormal below 1e-4).  8-bit weights: x and h are quantised by blocks of 128, as
+// mhc_fp8_quant does, when a segment's rows are brought to shared memory; each block's
+// product is scaled into fp32 sums.
 //
 // A slot's row of y is written once and a token's slots are added up in their
 // order, so nothing depends on which block did what.  (The last block at a tile of
@@ -51,7 +55,7 @@ constexpr int kPiece = 128;               // bytes of k a warp takes at once
 enum : int { kFaultExpert = 202 };
 
 struct FewP {
-    const void *x;        // up: [T, C] rows; down: h
+    const void *x;        // [T, C]
     const int32_t *ids;
     const float *w;
     const void *wt;       // weights [E, rows, K]
@@ -60,7 +64,7 @@ struct FewP {
     int T, k, E;
     int ntiles;           // tiles of an expert
     int wk;               // warps that split a tile's k
-    void *h;              // [T*k, F] fp32, or two terms of the type
+    float *h;             // [T*k, F]
     float *y;             // [T*k, C]
     int64_t F, C;
     int *fault;
@@ -110,6 +114,79 @@ __device__ __forceinline__ uint2 widen_e4m3(uint32_t w)
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i)
 {
     return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// h in terms of the weights' type: 8 consecutive values v of one of the 8 columns (the four
+// lanes of a quad hold 32), whose terms' sum is v times the power of two whose inverse is
+// returned.  An infinity is its first term alone (inf - inf would make it a NaN); a step that
+// holds one is rare.
+constexpr float kLargest = 3.4028235e38f;  // of fp32
+
+__device__ __forceinline__ float largest8(const float (&v)[8])
+{
+    return fmaxf(fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3]))),
+                 fmaxf(fmaxf(fabsf(v[4]), fabsf(v[5])), fmaxf(fabsf(v[6]), fabsf(v[7]))));
+}
+__device__ __forceinline__ f32x2 rest2(f32x2 v, float lo, float hi)  // v - (lo, hi)
+{
+    return f2_fma(f2_make(lo, hi), f2_make(-1.f, -1.f), v);
+}
+__device__ __forceinline__ float cut16(float v)
+{
+    return __uint_as_float(__float_as_uint(v) & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t tops(float lo, float hi)
+{
+    return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+__device__ __forceinline__ float split8(const float (&v)[8], uint32_t (&t)[3][4], const bf16 *)
+{
+    const bool infinite = __any_sync(kFull, largest8(v) > kLargest);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // cut, not rounded: what is left is exact and fits
+        float x = v[2 * i], y = v[2 * i + 1];
+        t[0][i] = tops(x, y);
+        f32x2 r = rest2(f2_make(x, y), cut16(x), cut16(y));
+        if (infinite) {
+            const float a = fabsf(x) > kLargest ? 0.f : x - cut16(x);
+            r = f2_make(a, fabsf(y) > kLargest ? 0.f : y - cut16(y));
+        }
+        f2_split(r, x, y);
+        t[1][i] = tops(x, y);
+        f2_split(rest2(r, cut16(x), cut16(y)), x, y);
+        t[2][i] = tops(x, y);
+    }
+    return 1.f;
+}
+__device__ __forceinline__ float split8(const float (&v)[8], uint32_t (&t)[2][4], const fp16 *)
+{
+    const fp16 *type = nullptr;
+    float m = largest8(v);
+    const bool infinite = __any_sync(kFull, m > kLargest);
+    if (infinite) {
+        m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]) > kLargest ? 0.f : fabsf(v[i]));
+    }
+    m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+    const uint32_t e = max(__float_as_uint(m) >> 23, 15u);
+    const float up = __uint_as_float((268u - e) << 23);  // 2^(141 - e)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const f32x2 s = f2_mul(f2_make(v[2 * i], v[2 * i + 1]), f2_make(up, up));
+        float x, y, x0, y0;
+        f2_split(s, x, y);
+        t[0][i] = round2(x, y, type);
+        widen2(t[0][i], x0, y0, type);
+        f2_split(rest2(s, x0, y0), x, y);
+        if (infinite) {
+            x = fabsf(x0) > kLargest ? 0.f : x;
+            y = fabsf(y0) > kLargest ? 0.f : y;
+        }
+        t[1][i] = round2(x, y, type);
+    }
+    return __uint_as_float((e - 14u) << 23);
 }
 
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
@@ -335,8 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
                 float v[4] = {0.f, 0.f, 0.f, 0.f};
                 if (k0 < p.K) {
                     if constexpr (DOWN) {
-                        const float4 u = __ldcg(reinterpret_cast<const float4 *>(
-                            static_cast<const float *>(p.h) + int64_t(slot) * p.K + k0));
+                        const float4 u =
+                            __ldcg(reinterpret_cast<const float4 *>(p.h + int64_t(slot) * p.K + k0));
                         v[0] = u.x;
                         v[1] = u.y;
                         v[2] = u.z;
@@ -360,16 +437,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
         }
         // columns of the operand without a slot repeat the first: nobody reads their sums
         const int bt = g < ns ? g : 0, bslot = slots[s0 + bt];
-        const uint8_t *bx[2];  // 16 bits: x, or the two terms of h
-        uint32_t bs = 0;       // 8 bits: the row in shared memory
+        const uint8_t *bx;   // 16 bits: x
+        const float *bh;     // and h
+        uint32_t bs = 0;     // 8 bits: the row in shared memory
         if constexpr (EIGHT) {
             bs = uint32_t(__cvta_generic_to_shared(xs + bt * xpitch + tig * 16));
         } else if constexpr (DOWN) {
-            const uint8_t *hh = static_cast<const uint8_t *>(p.h);
-            bx[0] = hh + bslot * Kb + tig * 16;
-            bx[1] = hh + (int64_t(n) + bslot) * Kb + tig * 16;
+            bh = p.h + bslot * p.K + tig * 8;
         } else {
-            bx[0] = static_cast<const uint8_t *>(p.x) + int64_t(bslot / p.k) * Kb + tig * 16;
+            bx = static_cast<const uint8_t *>(p.x) + int64_t(bslot / p.k) * Kb + tig * 16;
         }
         float acc[2][4];
         auto clear = [&]() {
@@ -411,26 +487,68 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
                     acc[m][3] = fmaf(part[m][3], q1, acc[m][3]);
                 }
             } else {
-                constexpr int TERMS = DOWN ? 2 : 1;
-                uint4 x[TERMS][2];
-#pragma unroll
-                for (int q = 0; q < TERMS; ++q)
+                float4 hv[DOWN ? 2 : 1][2];  // both steps' values on their way together
+                if constexpr (DOWN) {
 #pragma unroll
                     for (int st = 0; st < 2; ++st) {
-                        x[q][st] = zero4();
-                        if (off + st * 64 + tig * 16 < Kb)
-                            x[q][st] = *reinterpret_cast<const uint4 *>(bx[q] + off + st * 64);
-                    }
-#pragma unroll
-                for (int q = 0; q < TERMS; ++q)
-#pragma unroll
-                    for (int st = 0; st < 2; ++st)
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const uint4 u = b.a[st][2 * m], v = b.a[st][2 * m + 1];
-                            mma8<W, false>(acc[m], u.x, v.x, u.y, v.y, x[q][st].x, x[q][st].y);
-                            mma8<W, false>(acc[m], u.z, v.z, u.w, v.w, x[q][st].z, x[q][st].w);
+                        hv[st][0] = hv[st][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (off + st * 64 + tig * 16 < Kb) {
+                            const float *h = bh + (off >> 1) + st * 32;
+                            hv[st][0] = *reinterpret_cast<const float4 *>(h);
+                            hv[st][1] = *reinterpret_cast<const float4 *>(h + 4);
                         }
+                    }
+                }
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    if constexpr (DOWN) {
+                        constexpr bool SCALED = std::is_same<W, fp16>::value;
+                        constexpr int TERMS = SCALED ? 2 : 3;
+                        const float4 &lo = hv[st][0], &hi = hv[st][1];
+                        const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                        uint32_t x[TERMS][4];
+                        const float down = split8(v, x, static_cast<const W *>(nullptr));
+                        float part[2][4];
+                        float(&sum)[2][4] = SCALED ? part : acc;
+#pragma unroll
+                        for (int q = 0; q < TERMS; ++q)
+#pragma unroll
+                            for (int i = 0; i < 4; i += 2)  // two sums in turn
+#pragma unroll
+                                for (int m = 0; m < 2; ++m) {
+                                    const uint4 &u = b.a[st][2 * m], &w = b.a[st][2 * m + 1];
+                                    const uint32_t a0 = word(u, i), a1 = word(w, i);
+                                    const uint32_t a2 = word(u, i + 1), a3 = word(w, i + 1);
+                                    if (SCALED && q == 0 && i == 0)
+                                        mma8<W, true>(sum[m], a0, a1, a2, a3, x[q][i], x[q][i + 1]);
+                                    else
+                                        mma8<W, false>(sum[m], a0, a1, a2, a3, x[q][i], x[q][i + 1]);
+                                }
+                        if constexpr (SCALED) {  // of columns 2 tig and 2 tig + 1
+                            const float q0 = __shfl_sync(kFull, down, 8 * tig);
+                            const float q1 = __shfl_sync(kFull, down, 8 * tig + 4);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                acc[m][0] = fmaf(part[m][0], q0, acc[m][0]);
+                                acc[m][1] = fmaf(part[m][1], q1, acc[m][1]);
+                                acc[m][2] = fmaf(part[m][2], q0, acc[m][2]);
+                                acc[m][3] = fmaf(part[m][3], q1, acc[m][3]);
+                            }
+                        }
+                    } else {
+                        uint4 x = zero4();
+                        if (off + st * 64 + tig * 16 < Kb)
+                            x = *reinterpret_cast<const uint4 *>(bx + off + st * 64);
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2)
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                const uint4 &u = b.a[st][2 * m], &w = b.a[st][2 * m + 1];
+                                mma8<W, false>(acc[m], word(u, i), word(w, i), word(u, i + 1),
+                                               word(w, i + 1), word(x, i), word(x, i + 1));
+                            }
+                    }
+                }
             }
         };
         auto finish = [&](int tl) {
@@ -452,17 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
                         up += all[(w * TOK + t) * kPitch + 16 + r];
                     }
                     const float h = silu(gate, sigm(gate)) * up;
-                    const int slot = slots[s0 + t];
-                    const int64_t at = int64_t(slot) * p.F + int64_t(tl) * 16 + r;
-                    if constexpr (EIGHT) {
-                        static_cast<float *>(p.h)[at] = h;
-                    } else {
-                        X *hh = static_cast<X *>(p.h);
-                        const X top = X(h);
-                        const float rest = h - float(top);
-                        hh[at] = top;
-                        hh[int64_t(n) * p.F + at] = X(isfinite(rest) ? rest : 0.f);
-                    }
+                    p.h[int64_t(slots[s0 + t]) * p.F + int64_t(tl) * 16 + r] = h;
                 }
             } else {
                 for (int o = gtid; o < ns * 32; o += gsize) {
@@ -630,7 +738,7 @@ cudaError_t launch_moe_few(const MoeFewArgs &a, int dtype, int eight, cudaStream
     p.fault = a.fault;
     uint8_t *ws = static_cast<uint8_t *>(a.ws);
     const size_t n = size_t(a.T) * size_t(a.k);
-    p.h = ws;
+    p.h = reinterpret_cast<float *>(ws);
     p.y = reinterpret_cast<float *>(ws + n * size_t(a.F) * 4);
     if (eight) return dtype == 0 ? both<E4m3, bf16>(p, a, s) : both<E4m3, fp16>(p, a, s);
     return dtype == 0 ? both<bf16, bf16>(p, a, s) : both<fp16, fp16>(p, a, s);

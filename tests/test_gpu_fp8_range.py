@@ -1,0 +1,102 @@
+"""The 8-bit floating-point operators and the experts' layer for a few tokens at the ends of
+their range."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import _fp8 as F8
+from tests._edges import U, np64
+from tests._fp8 import E4M3, blocks
+from tests.test_gpu_fp8 import I32, few_case, few_ref, few_run, full
+
+pytestmark = pytest.mark.gpu
+HALVES = [torch.bfloat16, torch.float16]
+
+
+@pytest.fixture(scope="module")
+def M():
+    import layers_proj_rms_gb300 as m
+    yield m
+    assert m.mhc_device_error() == 0
+
+
+# ---- the activation between the two products of the few tokens' layer ---------
+
+def one_expert(gate, up, w2, x, dtype):
+    """One token, one expert, w = 1; gate and up [F, C], w2 [C, F], x [C], all exact in dtype."""
+    exact = x[None], torch.cat((gate, up))[None], w2[None]
+    x, w1, w2 = (t.to(dtype) for t in exact)
+    assert all(torch.equal(t.float(), e) for t, e in zip((x, w1, w2), exact))
+    return x, torch.zeros(1, 1, dtype=I32), torch.ones(1, 1), w1, None, w2, None
+
+
+def gate_of_64():
+    """silu(64) is 64 to the last bit of fp32, so h = 64 up where x[0] = 1."""
+    g = torch.zeros(16, 16)
+    g[:, 0] = 64.0
+    return g
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+def test_activation_keeps_the_bits_of_fp32(M, dtype):
+    """h[i] = 64 (1 + 85 2^-14 + i 2^-20), exact in fp32; f[i] = h[i] - h[0] = i 2^-14 without any
+    rounding."""
+    x, up, w2 = torch.zeros(16), torch.zeros(16, 16), torch.eye(16)
+    x[0], x[1] = 1.0, 2.0 ** -10
+    up[:, 0], up[:, 1], up[:, 2] = 1.0, torch.arange(16) * 2.0 ** -10, 85 / 16
+    x[2] = 2.0 ** -10
+    w2[:, 0] -= 1
+    f = few_run(M, one_expert(gate_of_64(), up, w2, x, dtype))
+    assert np64(f)[0].tolist() == [i * 2.0 ** -14 for i in range(16)]
+
+
+def test_small_fp16_activation_keeps_its_bits(M):
+    """h[i] = (1 + i / 256) 2^-24, which fp16 holds as its least number; times 2^12."""
+    x, up = torch.zeros(16), torch.zeros(16, 16)
+    x[0], x[1] = 1.0, 2.0 ** -14
+    up[:, 1] = (256 + torch.arange(16)) * 2.0 ** -24
+    f = few_run(M, one_expert(gate_of_64(), up, torch.eye(16) * 2.0 ** 12, x, torch.float16))
+    assert np64(f)[0].tolist() == [(1 + i / 256) * 2.0 ** -12 for i in range(16)]
+
+
+def test_large_fp16_activation_is_kept(M):
+    """h = 320 * 320 is above fp16's largest number, f = 16 h / 64 is not."""
+    x, w = torch.ones(16), torch.full((16, 16), 20.0)
+    f = few_run(M, one_expert(w, w, torch.full((16, 16), 1 / 64), x, torch.float16))
+    assert np64(f)[0].tolist() == [25600.0] * 16
+
+
+@pytest.mark.parametrize("T,C,F,E,k", [(1, 144, 400, 4, 2), (9, 272, 80, 3, 2), (30, 48, 1040, 4, 4)])
+@pytest.mark.parametrize("dtype", HALVES)
+def test_activations_of_all_sizes(M, T, C, F, E, k, dtype):
+    """Activations from 1e-7 to 1e6 beside one another in a row."""
+    x, ids, w, w1, s1, w2, s2 = few_case(T, C, F, E, k, dtype, False, 7 * T + F)
+    size = 10 ** (torch.rand(F, generator=torch.Generator().manual_seed(F)) * 13 - 7)
+    w1, w2 = w1.float(), w2.float()
+    w1[:, :F] *= 10
+    w1[:, F:] *= size[:, None].clamp(1e-3, 1e3)
+    w2 /= size.clamp(1e-3, 1e3)
+    case = (x, ids, w, w1.to(dtype), None, w2.to(dtype), None)
+    f = few_run(M, case)
+    assert f.isfinite().all()
+    F8.check_few(f, *few_ref(case))
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+def test_infinite_activation_beside_finite_ones(M, dtype):
+    """An infinity in h goes to f as itself, whatever stands beside it; a NaN as a NaN."""
+    x = torch.ones(1, 16)
+    w1 = torch.full((1, 32, 16), 20.0)
+    w1[0, 0] = math.inf
+    w2 = torch.zeros(1, 16, 16)
+    w2[0, :, 1] = -1.0           # of 102400
+    w2[0, :, 0] = 1.0            # of the infinity
+    w2[0, 8:, 0] = -1.0
+    w2[0, 15, 0] = 0.0
+    case = (x.to(dtype), torch.zeros(1, 1, dtype=I32), torch.ones(1, 1), w1.to(dtype), None,
+            w2.to(dtype), None)
+    f = np64(few_run(M, case))[0]
+    assert f[:8].tolist() == [math.inf] * 8 and f[8:15].tolist() == [-math.inf] * 7
+    assert math.isnan(f[15])
