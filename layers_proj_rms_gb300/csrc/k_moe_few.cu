@@ -454,6 +454,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[m][j] = 0.f;
         };
+        auto add = [&](const float (&part)[2][4], float q0, float q1) {  // times the columns' scales
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                acc[m][0] = fmaf(part[m][0], q0, acc[m][0]);
+                acc[m][1] = fmaf(part[m][1], q1, acc[m][1]);
+                acc[m][2] = fmaf(part[m][2], q0, acc[m][2]);
+                acc[m][3] = fmaf(part[m][3], q1, acc[m][3]);
+            }
+        };
         auto compute = [&](const Piece<EIGHT> &b, int pc) {
             const int off = pc * kPiece;
             if constexpr (EIGHT) {
@@ -487,67 +496,72 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
                     acc[m][3] = fmaf(part[m][3], q1, acc[m][3]);
                 }
             } else {
-                float4 hv[DOWN ? 2 : 1][2];  // both steps' values on their way together
+                // A piece's products have sums of their own, added with rounding to nearest: the tensor
+                // cores cut what they add to: along 16384 a bias of 6e-6 in fp16, 9e-7 in bf16.
                 if constexpr (DOWN) {
+                    constexpr bool SCALED = std::is_same<W, fp16>::value;
+                    constexpr int TERMS = SCALED ? 2 : 3;
+                    float4 h[2][2];  // both steps' values on their way together
 #pragma unroll
                     for (int st = 0; st < 2; ++st) {
-                        hv[st][0] = hv[st][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        h[st][0] = h[st][1] = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (off + st * 64 + tig * 16 < Kb) {
-                            const float *h = bh + (off >> 1) + st * 32;
-                            hv[st][0] = *reinterpret_cast<const float4 *>(h);
-                            hv[st][1] = *reinterpret_cast<const float4 *>(h + 4);
+                            const float *at = bh + (off >> 1) + st * 32;
+                            h[st][0] = *reinterpret_cast<const float4 *>(at);
+                            h[st][1] = *reinterpret_cast<const float4 *>(at + 4);
                         }
                     }
-                }
+                    float part[2][4];
 #pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    if constexpr (DOWN) {
-                        constexpr bool SCALED = std::is_same<W, fp16>::value;
-                        constexpr int TERMS = SCALED ? 2 : 3;
-                        const float4 &lo = hv[st][0], &hi = hv[st][1];
+                    for (int st = 0; st < 2; ++st) {
+                        const float4 lo = h[st][0], hi = h[st][1];
                         const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                         uint32_t x[TERMS][4];
                         const float down = split8(v, x, static_cast<const W *>(nullptr));
-                        float part[2][4];
-                        float(&sum)[2][4] = SCALED ? part : acc;
 #pragma unroll
-                        for (int q = 0; q < TERMS; ++q)
+                        for (int q = TERMS - 1; q >= 0; --q)  // the least term first
 #pragma unroll
-                            for (int i = 0; i < 4; i += 2)  // two sums in turn
+                            for (int i = 0; i < 4; i += 2)
 #pragma unroll
                                 for (int m = 0; m < 2; ++m) {
                                     const uint4 &u = b.a[st][2 * m], &w = b.a[st][2 * m + 1];
                                     const uint32_t a0 = word(u, i), a1 = word(w, i);
                                     const uint32_t a2 = word(u, i + 1), a3 = word(w, i + 1);
-                                    if (SCALED && q == 0 && i == 0)
-                                        mma8<W, true>(sum[m], a0, a1, a2, a3, x[q][i], x[q][i + 1]);
+                                    if ((SCALED || st == 0) && q == TERMS - 1 && i == 0)
+                                        mma8<W, true>(part[m], a0, a1, a2, a3, x[q][i], x[q][i + 1]);
                                     else
-                                        mma8<W, false>(sum[m], a0, a1, a2, a3, x[q][i], x[q][i + 1]);
+                                        mma8<W, false>(part[m], a0, a1, a2, a3, x[q][i], x[q][i + 1]);
                                 }
-                        if constexpr (SCALED) {  // of columns 2 tig and 2 tig + 1
-                            const float q0 = __shfl_sync(kFull, down, 8 * tig);
-                            const float q1 = __shfl_sync(kFull, down, 8 * tig + 4);
+                        if constexpr (SCALED)  // of columns 2 tig and 2 tig + 1
+                            add(part, __shfl_sync(kFull, down, 8 * tig),
+                                __shfl_sync(kFull, down, 8 * tig + 4));
+                    }
+                    if constexpr (!SCALED) add(part, 1.f, 1.f);
+                } else {
+                    uint4 x[2];
 #pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                acc[m][0] = fmaf(part[m][0], q0, acc[m][0]);
-                                acc[m][1] = fmaf(part[m][1], q1, acc[m][1]);
-                                acc[m][2] = fmaf(part[m][2], q0, acc[m][2]);
-                                acc[m][3] = fmaf(part[m][3], q1, acc[m][3]);
-                            }
-                        }
-                    } else {
-                        uint4 x = zero4();
+                    for (int st = 0; st < 2; ++st) {
+                        x[st] = zero4();
                         if (off + st * 64 + tig * 16 < Kb)
-                            x = *reinterpret_cast<const uint4 *>(bx + off + st * 64);
+                            x[st] = *reinterpret_cast<const uint4 *>(bx + off + st * 64);
+                    }
+                    float part[2][4];
+#pragma unroll
+                    for (int st = 0; st < 2; ++st)
 #pragma unroll
                         for (int i = 0; i < 4; i += 2)
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
                                 const uint4 &u = b.a[st][2 * m], &w = b.a[st][2 * m + 1];
-                                mma8<W, false>(acc[m], word(u, i), word(w, i), word(u, i + 1),
-                                               word(w, i + 1), word(x, i), word(x, i + 1));
+                                const uint32_t a0 = word(u, i), a1 = word(w, i);
+                                const uint32_t a2 = word(u, i + 1), a3 = word(w, i + 1);
+                                const uint32_t b0 = word(x[st], i), b1 = word(x[st], i + 1);
+                                if (st == 0 && i == 0)
+                                    mma8<W, true>(part[m], a0, a1, a2, a3, b0, b1);
+                                else
+                                    mma8<W, false>(part[m], a0, a1, a2, a3, b0, b1);
                             }
-                    }
+                    add(part, 1.f, 1.f);
                 }
             }
         };

@@ -100,3 +100,57 @@ def test_infinite_activation_beside_finite_ones(M, dtype):
     f = np64(few_run(M, case))[0]
     assert f[:8].tolist() == [math.inf] * 8 and f[8:15].tolist() == [-math.inf] * 7
     assert math.isnan(f[15])
+
+
+# ---- long sums ------------------------------------------------------------------
+
+def thirds(s, dtype):
+    """fp32 values as three of dtype, which hold all 24 bits."""
+    out = []
+    for _ in range(3):
+        out.append(s.to(dtype))
+        s = s - out[-1].float()
+    assert not s.any()
+    return torch.stack(out, -1)
+
+
+def long_sum_error(M, which, K, n, dtype):
+    """Of n sums of K positive products in the first (which = 1) or the second product: their
+    relative errors, found as the difference of two experts: the second one's sum is three terms,
+    the first one's rounded to fp32, which is exact; 64 of a gate of 64 is exact, too."""
+    g = torch.Generator().manual_seed(K + n)
+    C, F = (K, n) if which == 1 else (n, K)
+    x, w1, w2 = torch.ones(1, C), torch.zeros(2, 2 * F, C), torch.zeros(2, C, F)
+    w1[:, :F, 0] = 64.0
+    if which == 1:
+        x[0, 4:] = 1 + torch.rand(C - 4, generator=g)
+        x = x.to(dtype).float()
+        w1[0, F:] = (0.5 + torch.rand(F, C, generator=g)).to(dtype)
+        s = w1[0, F:].double() @ x[0].double()
+        w1[1, F:, 1:4] = thirds(s.float(), dtype).float()
+        w2[:, torch.arange(F), torch.arange(F)] = 1.0
+    else:
+        u = (0.5 + torch.rand(F, generator=g)).to(dtype)
+        w1[0, F:, 0] = u
+        w1[1, F:F + 3, 0] = 1.0
+        w2[0] = (0.5 + torch.rand(C, F, generator=g)).to(dtype)
+        s = w2[0].double() @ u.double()
+        w2[1, :, :3] = thirds(s.float(), dtype).float()
+    ids = torch.tensor([[0, 1]], dtype=I32)
+    f = few_run(M, (x.to(dtype), ids, torch.tensor([[1.0, -1.0]]), w1.to(dtype), None, w2.to(dtype),
+                    None))
+    f = f[0, :n].cpu().double() / 64
+    return (f - (s - s.float().double())) / s
+
+
+@pytest.mark.parametrize("which", [1, 2])
+@pytest.mark.parametrize("dtype", HALVES)
+def test_long_sums_are_rounded_to_nearest(M, which, dtype):
+    """Sums of 16384 products are right on the average.  Within a piece of 64 a tensor core cuts
+    what it adds to by 2^-23 of it at most, at most 8 times, while it grows to the piece's sum:
+    4.5 2^-23 of that; the pieces are added with rounding to nearest, which has no bias: 256
+    additions of a 16th of the sum at most, off by 2^-24 / sqrt(3) of it (rms), and the mean of
+    256 sums by a 16th of that, six times which is less than 2^-24."""
+    error = long_sum_error(M, which, 16384, 256, dtype)
+    assert abs(error.mean().item()) <= 10 * U
+    assert error.abs().max().item() <= (9 + 16 + 16) * U  # and none beyond what each addition may be
