@@ -88,7 +88,8 @@ MHC_API int mhc_version(void);
 
 /* Batch-invariant mode ([rlk] PR body: the fixed-K / batch-invariant GEMM
  * reference of task P1-2).  Off by default.  When on, the forward
- * projection's K splits are a function of K alone (4096-wide), so every
+ * projection's K splits are a function of K alone (4096-wide), as those of
+ * mhc_moe_few_fwd are of C and F alone, so every
  * per-token output of every op (H_*, u, r, y, out, dx, df, ...) is bitwise
  * independent of T and of the token's position in the batch; the sums over
  * tokens (dW, dalpha, db, dbias, dgamma) are deterministic for a given T.
@@ -634,7 +635,8 @@ MHC_API mhc_status mhc_fp8_wgrad(const uint8_t *at, mhc_fp8 format_a, const floa
  * s1 [E, blocks of C, blocks of 2F], s2 [E, blocks of F, blocks of C]; then x
  * and the activation are quantised to e4m3 by blocks of 128 as mhc_fp8_quant
  * does, the latter from its fp32 values.  Each slot's sums are fp32 throughout,
- * in an order that C, F, T k and E set: the other tokens' values do not matter.
+ * in an order that C, F, T k and E set, in batch-invariant mode C and F alone:
+ * the other tokens' values do not matter.
  * T <= 128, k <= 32, C and F multiples of 16 and <= 16384.
  * ws: mhc_workspace_bytes(MHC_OP_MOE_FEW_FWD, T, k, C + F). */
 MHC_API mhc_status mhc_moe_few_fwd(const void *x, mhc_dtype dtype, const int32_t *ids,

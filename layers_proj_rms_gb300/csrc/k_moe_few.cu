@@ -675,12 +675,15 @@ size_t few_smem(bool eight, int64_t K)
 // one token, 64 experts, 7168 x 2048, 8 bits: 82, 68, 68, 70, 75 (four); 64 tokens, 8
 // experts, 4096 x 14336, 16 bits: 809, 785, 791, 816, 872 (four); one token, 8 experts,
 // 1024 x 512, 8 bits: 14.2, 11.8, 10.4, 9.9, 10.1 (eight up, four down).
+// The number sets the order of a row's sums: it goes by kSplitSms, not by the device, and in
+// batch-invariant mode, where it must not go by the number of slots, by k alone.
 int split_of(int64_t K, int bytes, int64_t tiles)
 {
     const int64_t np = (K * bytes + kPiece - 1) / kPiece;
-    const double per_block = double(tiles) / num_sms();
+    const double per_block = double(tiles) / kSplitSms;
     int best = int(std::min<int64_t>(np, 4));
     best = best == 3 ? 2 : best;
+    if (batch_invariant()) return best;
     double least = 1e30;
     for (int w = best; w <= kWarps && w <= np; w *= 2) {
         const double turns = per_block * w / kWarps;

@@ -154,3 +154,23 @@ def test_long_sums_are_rounded_to_nearest(M, which, dtype):
     error = long_sum_error(M, which, 16384, 256, dtype)
     assert abs(error.mean().item()) <= 10 * U
     assert error.abs().max().item() <= (9 + 16 + 16) * U  # and none beyond what each addition may be
+
+
+# ---- batch-invariant mode ------------------------------------------------------
+
+@pytest.mark.parametrize("eight", [False, True])
+@pytest.mark.parametrize("C,F,E,k", [(1024, 512, 64, 2), (272, 1040, 8, 2), (4096, 176, 60, 4)])
+def test_batch_invariant_mode(M, C, F, E, k, eight):
+    """With the mode on a token's result has the same bits in every batch."""
+    x, ids, w, w1, s1, w2, s2 = few_case(100, C, F, E, k, torch.bfloat16, eight, C + F)
+    w1, s1, w2, s2 = (None if t is None else t.cuda() for t in (w1, s1, w2, s2))
+    M.mhc_set_batch_invariant(True)
+    try:
+        out = few_run(M, (x, ids, w, w1, s1, w2, s2))
+        F8.check_few(out, *few_ref((x, ids, w) + tuple(None if t is None else t.cpu()
+                                                       for t in (w1, s1, w2, s2))))
+        for lo, n in ((0, 1), (99, 1), (40, 2), (13, 17), (50, 50)):
+            one = few_run(M, (x[lo:lo + n], ids[lo:lo + n], w[lo:lo + n], w1, s1, w2, s2))
+            assert torch.equal(one, out[lo:lo + n]), (lo, n)
+    finally:
+        M.mhc_set_batch_invariant(False)
