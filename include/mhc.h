@@ -564,7 +564,9 @@ MHC_API mhc_status mhc_moe_combine_bwd(const void *df, const void *ys, mhc_dtype
 /* rows]) or for each 128 rows (s [blocks of K, blocks of rows]): it    */
 /* stands for q * s.  Sums are fp32: a block's products by the tensor   */
 /* cores, exact but for their sum's rounding, then scaled and added in  */
-/* fp32; each result is rounded to its type once.                       */
+/* fp32; each result is rounded to its type once.  Scales of any size   */
+/* may meet unless it says otherwise: no step overflows or loses bits   */
+/* unless the scaled product itself does.                               */
 /* Segments: offsets [G + 1] int32 as mhc_moe_sort writes them, or NULL */
 /* (G = 1): all R rows.  Offsets that go back or leave [0, R] are taken */
 /* as the nearest that do not, and set device error 205.                */

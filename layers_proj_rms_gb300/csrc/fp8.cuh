@@ -45,6 +45,16 @@ __device__ __forceinline__ float f8_up(uint32_t amax)
     return __fdiv_rn(f8_top<FMT>(), __uint_as_float(amax));
 }
 
+// Of two scales r and c and a sum d of products of 8-bit values (2^-32 <= |d| < 2^40, or 0):
+// whether r c is no normal number though neither is 0.  d is then multiplied by the larger
+// and that by the smaller: where |r c| > fp32's largest both are above 1, where it is below
+// its least normal number the larger is below 2^23, so no step overflows or loses bits
+// unless d r c does.
+__device__ __forceinline__ bool f8_apart(float r, float c)
+{
+    return f8_mag(r * c) - 0x00800000u >= 0x7f000000u && r != 0.f && c != 0.f;
+}
+
 // 1 / (1 + exp(-g)): 0 where exp(-g) is inf.  An exp(-g) that is no normal number may be
 // zero beside 1.  Both approximations are off by a unit or two of fp32 at most: over normal
 // gates the gradient is off by 5.6e-8 (rms), with expf and a divide by 5.8e-8.

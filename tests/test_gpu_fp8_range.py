@@ -174,3 +174,45 @@ def test_batch_invariant_mode(M, C, F, E, k, eight):
             assert torch.equal(one, out[lo:lo + n]), (lo, n)
     finally:
         M.mhc_set_batch_invariant(False)
+
+
+# ---- scales far apart ----------------------------------------------------------
+
+# exponents of the two operands' scales; whether the 8-bit values are the least ones
+SCALES = {"product past the largest": (70, 58, True), "product below the least": (-75, -70, False),
+          "first large": (112, -100, False), "first small": (-118, 100, True),
+          "second large": (-100, 112, False), "second small": (100, -118, True)}
+
+
+def eight_bits(g, least, *shape):
+    if least:  # subnormal: up to 7 / 512
+        return (torch.randint(-7, 8, shape, generator=g) * 2.0 ** -9).to(E4M3)
+    return (torch.randint(-28, 29, shape, generator=g) * 16.0).to(E4M3)
+
+
+def scales(g, e, *shape):
+    return (1 + torch.rand(*shape, generator=g)) * 2.0 ** e
+
+
+def check_scaled(out, ref, mag, K, what=""):
+    """fp32: the operations' roundings, the result's own, and the least subnormal."""
+    g = np64(out)
+    assert np.all(np.isfinite(g)), what
+    tol = (F8.product_ops(K) + 1) * U * mag + 2.0 ** -149
+    assert np.all(np.abs(g - ref) <= tol), (what, np.max(np.abs(g - ref) / (mag + 2.0 ** -149)))
+
+
+@pytest.mark.parametrize("R,N,K", [(130, 264, 272), (4000, 2824, 144)])
+@pytest.mark.parametrize("kind", SCALES)
+def test_gemm_of_scales_far_apart(M, R, N, K, kind):
+    ea, eb, least = SCALES[kind]
+    g = torch.Generator().manual_seed(R)
+    a, b = eight_bits(g, least, R, K), eight_bits(g, least, 1, N, K)
+    a[7] = 0  # of a row of zeros comes a row of zeros
+    sa, sb = scales(g, ea, blocks(K), R), scales(g, eb, 1, blocks(K), blocks(N))
+    sa[0, :5] = 1.5 * 2.0 ** -eb  # and some whose scales' product is near 1
+    out = full(R, N)
+    M.mhc_fp8_gemm(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), None, out)
+    av, bv = F8.values(a, sa), F8.values(b[0], sb[0])
+    check_scaled(out, av @ bv.T, np.abs(av) @ np.abs(bv).T, K, kind)
+    assert not out[7].any()
