@@ -216,3 +216,23 @@ def test_gemm_of_scales_far_apart(M, R, N, K, kind):
     av, bv = F8.values(a, sa), F8.values(b[0], sb[0])
     check_scaled(out, av @ bv.T, np.abs(av) @ np.abs(bv).T, K, kind)
     assert not out[7].any()
+
+
+# ---- the same of the weights' gradient --------------------------------------------
+
+@pytest.mark.parametrize("R,M_,N", [(272, 130, 264), (144, 4000, 2824)])
+@pytest.mark.parametrize("kind", SCALES)
+def test_wgrad_of_scales_far_apart(M, R, M_, N, kind):
+    """Of any size, but the first ones within [2^-94, 2^88]."""
+    ea, eb, least = SCALES[kind]
+    near = lambda e: min(max(e, -94), 87)  # noqa: E731
+    g = torch.Generator().manual_seed(R)
+    at, bt = eight_bits(g, least, M_, R), eight_bits(g, least, N, R)
+    at[7], bt[9] = 0, 0
+    sat, sbt = scales(g, near(ea), blocks(R), M_), scales(g, eb, blocks(R), N)
+    sat[0, :5] = 1.5 * 2.0 ** near(-eb)
+    out = full(1, M_, N)
+    M.mhc_fp8_wgrad(at.cuda(), sat.cuda(), bt.cuda(), sbt.cuda(), None, out)
+    av, bv = F8.values(at, sat), F8.values(bt, sbt)
+    check_scaled(out[0], av @ bv.T, np.abs(av) @ np.abs(bv).T, R, kind)
+    assert not out[0, 7].any() and not out[0, :, 9].any()
