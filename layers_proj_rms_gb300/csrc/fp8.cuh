@@ -54,6 +54,17 @@ __device__ __forceinline__ bool f8_apart(float r, float c)
 {
     return f8_mag(r * c) - 0x00800000u >= 0x7f000000u && r != 0.f && c != 0.f;
 }
+// d r c so
+__device__ __forceinline__ float f8_scaled(float d, float r, float c)
+{
+    if (!f8_apart(r, c)) return d * (r * c);
+    return fabsf(r) > fabsf(c) ? d * r * c : d * c * r;
+}
+// Whether d r may be no normal number: |r| < 2^-94 or > 2^88.
+__device__ __forceinline__ bool f8_far(float r)
+{
+    return f8_mag(r) - 0x10800000u > 0x5b000000u && r != 0.f;
+}
 
 // 1 / (1 + exp(-g)): 0 where exp(-g) is inf.  An exp(-g) that is no normal number may be
 // zero beside 1.  Both approximations are off by a unit or two of fp32 at most: over normal

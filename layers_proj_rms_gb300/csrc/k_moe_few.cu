@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
             pdl_wait();
             waited = true;
         }
+        bool far = false;  // whether a row's scale is one that needs care
         if constexpr (EIGHT) {
             // the segment's rows, quantised, to shared memory
             __syncthreads();
@@ -424,16 +425,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
                         widen<X, 4>(u, v);
                     }
                 }
-                uint32_t m = kLeastBits;
+                uint32_t m = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) m = max(m, f8_mag(v[j]));
                 m = __reduce_max_sync(kFull, m);
+                const bool zeros = m == 0;
+                m = max(m, kLeastBits);
                 const float up = f8_up<0>(m);
                 *reinterpret_cast<uint32_t *>(xs + t * xpitch + kb * kFp8Block + lane * 4) =
                     f8_cvt4<0>(v[0] * up, v[1] * up, v[2] * up, v[3] * up);
-                if (lane == 0) sx[kb * TOK + t] = f8_scale<0>(m);
+                const float scale = f8_scale<0>(m);
+                far |= f8_far(scale) && !zeros;
+                if (lane == 0) sx[kb * TOK + t] = scale;
             }
-            __syncthreads();
+            far = __syncthreads_or(far);
         }
         // columns of the operand without a slot repeat the first: nobody reads their sums
         const int bt = g < ns ? g : 0, bslot = slots[s0 + bt];
@@ -487,13 +492,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
                     }
                 }
                 const float2 q = *reinterpret_cast<const float2 *>(sx + pc * TOK + 2 * tig);
+                if (far) {
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float q0 = q.x * b.s[m], q1 = q.y * b.s[m];
-                    acc[m][0] = fmaf(part[m][0], q0, acc[m][0]);
-                    acc[m][1] = fmaf(part[m][1], q1, acc[m][1]);
-                    acc[m][2] = fmaf(part[m][2], q0, acc[m][2]);
-                    acc[m][3] = fmaf(part[m][3], q1, acc[m][3]);
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[m][j] += f8_scaled(part[m][j], j & 1 ? q.y : q.x, b.s[m]);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        acc[m][0] = fmaf(part[m][0] * q.x, b.s[m], acc[m][0]);
+                        acc[m][1] = fmaf(part[m][1] * q.y, b.s[m], acc[m][1]);
+                        acc[m][2] = fmaf(part[m][2] * q.x, b.s[m], acc[m][2]);
+                        acc[m][3] = fmaf(part[m][3] * q.y, b.s[m], acc[m][3]);
+                    }
                 }
             } else {
                 // A piece's products have sums of their own, added with rounding to nearest: the tensor

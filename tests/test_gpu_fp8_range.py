@@ -236,3 +236,46 @@ def test_wgrad_of_scales_far_apart(M, R, M_, N, kind):
     av, bv = F8.values(at, sat), F8.values(bt, sbt)
     check_scaled(out[0], av @ bv.T, np.abs(av) @ np.abs(bv).T, R, kind)
     assert not out[0, 7].any() and not out[0, :, 9].any()
+
+
+# ---- scales of the few tokens' layer ---------------------------------------------
+
+def test_few_zeros_under_large_scales(M):
+    """Weights of zeros give zeros, however large the scales' product is."""
+    x = (torch.rand(3, 144) + 1).bfloat16() * 2.0 ** 80
+    w1, s1 = torch.zeros(2, 64, 144).to(E4M3), torch.full((2, 2, 1), 2.0 ** 60)
+    w2, s2 = torch.ones(2, 144, 32).to(E4M3), torch.ones(2, 1, 2)
+    ids = torch.tensor([[0], [1], [1]], dtype=I32)
+    assert not few_run(M, (x, ids, torch.ones(3, 1), w1, s1, w2, s2)).any()
+
+
+def test_few_small_scales(M):
+    """h is 2^-60, the second product's scales 2^-76: of their product fp32 holds four bits."""
+    T, C, F = 3, 144, 128
+    g = torch.Generator().manual_seed(3)
+    x = (torch.rand(T, C, generator=g) + 1).bfloat16()
+    w1 = torch.cat((torch.full((1, F, C), 0.5), torch.rand(1, F, C, generator=g) + 0.5), 1)
+    s1 = torch.ones(1, blocks(C), 2)
+    s1[:, :, 1] = 2.0 ** -73  # up
+    w2, s2 = (torch.rand(1, C, F, generator=g) * 400 + 40).to(E4M3), scales(g, -76, 1, 1, blocks(C))
+    case = (x, torch.zeros(T, 1, dtype=I32), torch.ones(T, 1), w1.to(E4M3), s1, w2, s2)
+    f, err = few_ref(case)
+    out = np64(few_run(M, case))
+    assert np.abs(f).min() > 2.0 ** -125  # bf16's normal numbers
+    assert np.all(np.abs(out - f) <= err + 2.0 ** -8 * (np.abs(f) + err))
+
+
+def test_few_large_rows(M):
+    """Rows of 2^121 under weights of 2^-125: a block's sum times the row's scale is past fp32."""
+    T, C, F = 5, 272, 80
+    g = torch.Generator().manual_seed(4)
+    x = ((torch.rand(T, C, generator=g) + 1) * 2.0 ** 121).bfloat16()
+    x[3] *= 2.0 ** -121
+    w1 = torch.randint(-28, 29, (1, 2 * F, C), generator=g).float().to(E4M3)
+    s1 = scales(g, -125, 1, blocks(C), 2)
+    w2, s2 = eight_bits(g, False, 1, C, F), scales(g, -12, 1, 1, blocks(C))
+    case = (x, torch.zeros(T, 1, dtype=I32), torch.ones(T, 1), w1, s1, w2, s2)
+    f, err = few_ref(case)
+    out = few_run(M, case)
+    assert out.isfinite().all() and np.abs(f).max() > 1
+    assert np.all(np.abs(np64(out) - f) <= err + 2.0 ** -8 * (np.abs(f) + err) + 2.0 ** -126)
