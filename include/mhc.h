@@ -604,9 +604,10 @@ MHC_API mhc_status mhc_fp8_swiglu_bwd(const void *da, const void *h, mhc_dtype d
                                       uint8_t *qt, float *st, mhc_stream_t stream);
 
 /* out [R, N]: out[r][n] = sum_k a[r][k] b[e][n][k] for the rows r of segment
- * e; rows of no segment are zeroed and not read.  a [R, K] with sa [blocks of
- * K, R]; b [G, N, K] with sb [G, blocks of K, blocks of N].  The gradient of
- * the rows is the same product with the transposed weights (qt, st of tiles).
+ * e; rows of no segment are zeroed (what a and sa hold for them is not used).
+ * a [R, K] with sa [blocks of K, R]; b [G, N, K] with sb [G, blocks of K, blocks
+ * of N].  The gradient of the rows is the same product with the transposed
+ * weights (qt, st of tiles).
  * N a multiple of 8, K of 16, G <= MHC_MOE_MAX_EXPERTS, R <= 2^31 - 128.  A row's
  * result does not depend on the other rows or on R. */
 MHC_API mhc_status mhc_fp8_gemm(const uint8_t *a, mhc_fp8 format_a, const float *sa,

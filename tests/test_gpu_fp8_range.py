@@ -7,9 +7,10 @@ import pytest
 import torch
 
 from tests import _fp8 as F8
-from tests._edges import U, np64
-from tests._fp8 import E4M3, blocks
-from tests.test_gpu_fp8 import I32, few_case, few_ref, few_run, full
+from tests._edges import U, check, np64
+from tests._fp8 import E4M3, E5M2, blocks
+from tests.test_gpu_fp8 import (I32, few_case, few_ref, few_run, full, gemm_case, wgrad_case,
+                                wgrad_ref)
 
 pytestmark = pytest.mark.gpu
 HALVES = [torch.bfloat16, torch.float16]
@@ -279,3 +280,17 @@ def test_few_large_rows(M):
     out = few_run(M, case)
     assert out.isfinite().all() and np.abs(f).max() > 1
     assert np.all(np.abs(np64(out) - f) <= err + 2.0 ** -8 * (np.abs(f) + err) + 2.0 ** -126)
+
+
+# ---- rows of no segment -----------------------------------------------------------
+
+def test_gemm_rows_behind_a_segment_are_not_used(M):
+    """Rows of no segment may hold anything: an infinity and a NaN among the values and scales."""
+    a, sa, b, sb, off, R = gemm_case([100, 60], 1, 64, 144, E5M2, E4M3, 3, 96)
+    want, out = full(R, 64), full(R, 64)
+    M.mhc_fp8_gemm(*(t.cuda() for t in (a, sa, b, sb, off)), want)
+    raw = a.view(torch.uint8)
+    raw[160:] = torch.tensor([0x7c, 0x7f, 0xfc, 0x7b], dtype=torch.uint8).repeat(36)
+    sa[:, 160::2], sa[:, 161::2] = math.inf, 0.0
+    M.mhc_fp8_gemm(*(t.cuda() for t in (a, sa, b, sb, off)), out)
+    assert torch.equal(out, want) and not out[160:].any() and out.isfinite().all()
