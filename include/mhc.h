@@ -618,10 +618,12 @@ MHC_API mhc_status mhc_fp8_gemm(const uint8_t *a, mhc_fp8 format_a, const float 
 /* out [G, M, N]: out[e][m][n] = sum over the rows r of segment e of
  * at[m][r] bt[n][r], zero for an empty segment.  at [M, R] with sat [blocks
  * of R, M], bt [N, R] with sbt [blocks of R, N] (qt, st of the rows' two
- * matrices).  Segments start at multiples of 128 (sort with align 128; others
- * are rounded down and set device error 206).  A block's sum is multiplied by sat,
- * then by sbt: sat above 2^88 may overflow, below 2^-94 lose bits, in between.
- * N a multiple of 8, R of 16, R <= 2^31 - 128. */
+ * matrices).  Every offset, the last one too, is a multiple of 128 or R (sort
+ * with align 128; others are rounded down, so that rows are lost, and set device
+ * error 206); all rows of a segment count, those behind its slots must be zeros.
+ * A block's sum is multiplied by sat, then by sbt: sat above 2^88 may overflow,
+ * below 2^-94 lose bits, in between.  N a multiple of 8, R of 16,
+ * R <= 2^31 - 128. */
 MHC_API mhc_status mhc_fp8_wgrad(const uint8_t *at, mhc_fp8 format_a, const float *sat,
                                  const uint8_t *bt, mhc_fp8 format_b, const float *sbt,
                                  const int32_t *offsets, int64_t G, int64_t R, int64_t M,

@@ -282,6 +282,23 @@ def test_few_large_rows(M):
     assert np.all(np.abs(np64(out) - f) <= err + 2.0 ** -8 * (np.abs(f) + err) + 2.0 ** -126)
 
 
+# ---- segments' ends ---------------------------------------------------------------
+
+@pytest.mark.parametrize("last,as_if", [(200, 128), (256, 256), (272, 272), (127, 0), (271, 256)])
+def test_wgrad_of_a_last_end_off_the_blocks(M, last, as_if):
+    """Any offset, the last one too, that is neither a multiple of 128 nor R is rounded down to
+    one, and reported."""
+    at, sat, bt, sbt, _ = wgrad_case([272], 40, 64, E4M3, E4M3, 5, 112)
+    at, bt, sat, sbt = at[:, :272].clone(), bt[:, :272].clone(), sat[:3].clone(), sbt[:3].clone()
+    sat = sat.nan_to_num(0.5)
+    off = torch.tensor([0, last], dtype=I32)
+    out = full(1, 40, 64)
+    M.mhc_fp8_wgrad(*(t.cuda() for t in (at, sat, bt, sbt, off)), out)
+    assert M.mhc_device_error() == (206 if last != as_if else 0)
+    ref, mag = wgrad_ref(at, sat, bt, sbt, torch.tensor([0, as_if]))
+    check(out, ref, mag, F8.product_ops(272))
+
+
 # ---- rows of no segment -----------------------------------------------------------
 
 def test_gemm_rows_behind_a_segment_are_not_used(M):
