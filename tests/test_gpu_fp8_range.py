@@ -311,3 +311,75 @@ def test_gemm_rows_behind_a_segment_are_not_used(M):
     sa[:, 160::2], sa[:, 161::2] = math.inf, 0.0
     M.mhc_fp8_gemm(*(t.cuda() for t in (a, sa, b, sb, off)), out)
     assert torch.equal(out, want) and not out[160:].any() and out.isfinite().all()
+
+
+# ---- offsets past 32 bits ---------------------------------------------------------
+
+def random_bits(*shape, small=False):
+    """Finite e4m3 values of every sign and exponent, or such up to 2, made on the device."""
+    v = torch.empty(*shape, dtype=torch.uint8, device="cuda").random_(0, 0x40 if small else 0x7e)
+    return v.view(E4M3)
+
+
+def test_wgrad_past_32_bits(M):
+    """The results of the last of 17 segments stand past 2^32 elements."""
+    G, M_, N = 17, 16384, 16392
+    R = 128 * G
+    at, bt = random_bits(M_, R), random_bits(N, R)
+    sat = torch.rand(G, M_, device="cuda") + 0.5
+    sbt = torch.rand(G, N, device="cuda") + 0.5
+    off = torch.arange(G + 1, dtype=I32, device="cuda") * 128
+    out = torch.full((G, M_, N), math.nan, dtype=torch.bfloat16, device="cuda")
+    M.mhc_fp8_wgrad(at, sat, bt, sbt, off, out)
+    for e in (0, G - 1):
+        rows_ = slice(128 * e, 128 * e + 128)
+        one = torch.full((1, M_, N), math.nan, dtype=torch.bfloat16, device="cuda")
+        M.mhc_fp8_wgrad(at[:, rows_].contiguous(), sat[e:e + 1], bt[:, rows_].contiguous(),
+                        sbt[e:e + 1], None, one)
+        assert torch.equal(out[e], one[0]) and one.isfinite().all() and one.any()
+
+
+def test_gemm_rows_past_32_bits(M):
+    """R N past 2^32: the last segment ends inside a tile and a box, rows of no segment follow."""
+    N, K = 16392, 144
+    R = 262272 + 99
+    end = R - 70
+    a, b = random_bits(R, K), random_bits(2, N, K, small=True)
+    sa = torch.rand(blocks(K), R, device="cuda") + 0.5
+    sb = torch.rand(2, blocks(K), blocks(N), device="cuda") + 0.5
+    off = torch.tensor([0, 262000, end], dtype=I32, device="cuda")
+    out = torch.full((R, N), math.nan, dtype=torch.bfloat16, device="cuda")
+    M.mhc_fp8_gemm(a, sa, b, sb, off, out)
+    lo = end - 130
+    one = torch.full((130, N), math.nan, dtype=torch.bfloat16, device="cuda")
+    M.mhc_fp8_gemm(a[lo:end], sa[:, lo:end].contiguous(), b[1:], sb[1:].clone(), None, one)
+    assert torch.equal(out[lo:end], one) and one.isfinite().all() and one.any()
+    assert not out[end:].any()
+    assert not out[:end].isnan().any(1).any()
+
+
+@pytest.mark.parametrize("way", ["fwd", "bwd"])
+def test_swiglu_past_32_bits(M, way):
+    """R 2F past 2^32: the last rows, and the last columns of the transposed copy."""
+    R, F = 262272, 8208
+    h = torch.empty(R, 2 * F, dtype=torch.bfloat16, device="cuda").normal_()
+    da = torch.empty(R, F, dtype=torch.bfloat16, device="cuda").normal_() if way == "bwd" else None
+    C = F if way == "fwd" else 2 * F
+
+    def run(h, da):
+        n = h.shape[0]
+        y = torch.full((n, C), math.nan, dtype=torch.bfloat16, device="cuda")
+        q, qt = (torch.full(s, 0x7f, dtype=torch.uint8, device="cuda").view(E4M3)
+                 for s in ((n, C), (C, n)))
+        s, st = full(blocks(C), n), full(blocks(n), C)
+        if way == "fwd":
+            M.mhc_fp8_swiglu_fwd(h, y, q, s, qt, st)
+        else:
+            M.mhc_fp8_swiglu_bwd(da, h, y, q, s, qt, st)
+        return y, q.view(torch.uint8), s, qt.view(torch.uint8), st
+
+    y, q, s, qt, st = run(h, da)
+    ty, tq, ts, tqt, tst = run(h[-128:].clone(), da[-128:].clone() if way == "bwd" else None)
+    assert torch.equal(y[-128:], ty) and torch.equal(q[-128:], tq) and torch.equal(s[:, -128:], ts)
+    assert torch.equal(qt[:, -128:], tqt) and torch.equal(st[-1:], tst)
+    assert ty.isfinite().all() and ty.any()
