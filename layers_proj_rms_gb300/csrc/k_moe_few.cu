@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
             pdl_wait();
             waited = true;
         }
-        bool far = false;  // whether a row's scale is one that needs care
+        bool far = false;  // whether a scale of the segment's rows is one that needs care
         if constexpr (EIGHT) {
             // the segment's rows, quantised, to shared memory
             __syncthreads();
@@ -492,21 +492,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_moe_few(const FewP p)
                     }
                 }
                 const float2 q = *reinterpret_cast<const float2 *>(sx + pc * TOK + 2 * tig);
-                if (far) {
+                auto scaled = [&](auto care) {
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[m][j] += f8_scaled(part[m][j], j & 1 ? q.y : q.x, b.s[m]);
-                } else {
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        acc[m][0] = fmaf(part[m][0] * q.x, b.s[m], acc[m][0]);
-                        acc[m][1] = fmaf(part[m][1] * q.y, b.s[m], acc[m][1]);
-                        acc[m][2] = fmaf(part[m][2] * q.x, b.s[m], acc[m][2]);
-                        acc[m][3] = fmaf(part[m][3] * q.y, b.s[m], acc[m][3]);
-                    }
-                }
+                        for (int j = 0; j < 4; ++j) {
+                            const float r = j & 1 ? q.y : q.x;
+                            // by the column's own scale: the others keep their bits
+                            if (decltype(care)::value && f8_far(r))
+                                acc[m][j] += f8_scaled(part[m][j], r, b.s[m]);
+                            else
+                                acc[m][j] = fmaf(part[m][j] * r, b.s[m], acc[m][j]);
+                        }
+                };
+                if (far)
+                    scaled(std::true_type());
+                else
+                    scaled(std::false_type());
             } else {
                 // A piece's products have sums of their own, added with rounding to nearest: the tensor
                 // cores cut what they add to: along 16384 a bias of 6e-6 in fp16, 9e-7 in bf16.

@@ -383,3 +383,20 @@ def test_swiglu_past_32_bits(M, way):
     assert torch.equal(y[-128:], ty) and torch.equal(q[-128:], tq) and torch.equal(s[:, -128:], ts)
     assert torch.equal(qt[:, -128:], tqt) and torch.equal(st[-1:], tst)
     assert ty.isfinite().all() and ty.any()
+
+
+# ---- other tokens of a segment ----------------------------------------------------
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("eight", [False, True])
+def test_few_bits_beside_a_token_out_of_range(M, dtype, eight):
+    """A token that holds an infinity, a NaN or the type's largest number leaves the bits of the
+    seven beside it as they are."""
+    case = few_case(8, 1040, 2048, 1, 1, dtype, eight, 5, 0.0)
+    out = few_run(M, case)
+    for v in (math.inf, math.nan, torch.finfo(dtype).max):
+        x = case[0].clone()
+        x[5, 3] = v
+        again = few_run(M, (x,) + case[1:])
+        keep = torch.arange(8, device="cuda") != 5
+        assert torch.equal(again[keep], out[keep]), v
