@@ -25,7 +25,8 @@
 // fp16, two of the values times a power of two that brings the largest of the 32 that a
 // column has in a step to [2^14, 2^15), undone in the fp32 sums: off by 2^-23 of the
 // value or 2^-40 of that largest (unscaled terms overflow at 65504 and are
-// subnormal below 1e-4).  8-bit weights: x and h are quantised by blocks of 128, as
+// subnormal below 1e-4).  A term more than 16 bits of h need, and sums of their own for each
+// piece (see there), take 199 us for 190 at 13 tokens of 60 experts, 4096 x 1408.  8-bit weights: x and h are quantised by blocks of 128, as
 // mhc_fp8_quant does, when a segment's rows are brought to shared memory; each block's
 // product is scaled into fp32 sums.
 //
@@ -139,22 +140,29 @@ __device__ __forceinline__ uint32_t tops(float lo, float hi)
 {
     return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
+template <bool INFINITE>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[3][4], int i)
+{
+    // cut, not rounded: what is left is exact and fits
+    t[0][i] = tops(x, y);
+    f32x2 r = rest2(f2_make(x, y), cut16(x), cut16(y));
+    if constexpr (INFINITE) {
+        const float a = fabsf(x) > kLargest ? 0.f : x - cut16(x);
+        r = f2_make(a, fabsf(y) > kLargest ? 0.f : y - cut16(y));
+    }
+    f2_split(r, x, y);
+    t[1][i] = tops(x, y);
+    f2_split(rest2(r, cut16(x), cut16(y)), x, y);
+    t[2][i] = tops(x, y);
+}
 __device__ __forceinline__ float split8(const float (&v)[8], uint32_t (&t)[3][4], const bf16 *)
 {
-    const bool infinite = __any_sync(kFull, largest8(v) > kLargest);
+    if (__any_sync(kFull, largest8(v) > kLargest)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {  // cut, not rounded: what is left is exact and fits
-        float x = v[2 * i], y = v[2 * i + 1];
-        t[0][i] = tops(x, y);
-        f32x2 r = rest2(f2_make(x, y), cut16(x), cut16(y));
-        if (infinite) {
-            const float a = fabsf(x) > kLargest ? 0.f : x - cut16(x);
-            r = f2_make(a, fabsf(y) > kLargest ? 0.f : y - cut16(y));
-        }
-        f2_split(r, x, y);
-        t[1][i] = tops(x, y);
-        f2_split(rest2(r, cut16(x), cut16(y)), x, y);
-        t[2][i] = tops(x, y);
+        for (int i = 0; i < 4; ++i) split2<true>(v[2 * i], v[2 * i + 1], t, i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split2<false>(v[2 * i], v[2 * i + 1], t, i);
     }
     return 1.f;
 }
@@ -685,10 +693,11 @@ size_t few_smem(bool eight, int64_t K)
 // leave warps without a tile where a block has few.  So the least of tiles in
 // turn x (pieces of a warp + 2), for as many segments as the slots can make; but
 // four at least, whose pieces are 512 bytes in a row.  With one, two, four, eight and 16:
-// 13 tokens, 60 experts, 4096 x 1408, 16 bits: 249, 209, 190, 183, 195 us (four are taken);
-// one token, 64 experts, 7168 x 2048, 8 bits: 82, 68, 68, 70, 75 (four); 64 tokens, 8
-// experts, 4096 x 14336, 16 bits: 809, 785, 791, 816, 872 (four); one token, 8 experts,
-// 1024 x 512, 8 bits: 14.2, 11.8, 10.4, 9.9, 10.1 (eight up, four down).
+// 13 tokens, 60 experts, 4096 x 1408, 16 bits: 266, 220, 199, 192, 215 us (four are taken,
+// 3% from the best); one token, 64 experts, 7168 x 2048, 8 bits: 84, 69, 68, 71, 75 (four),
+// 16 bits: 147, 125, 122, 127, 130 (four); 64 tokens, 8 experts, 4096 x 14336, 16 bits: 865,
+// 840, 843, 871, 929 (four); one token, 8 experts, 1024 x 512, 8 bits: 14.7, 12.2, 10.6,
+// 10.2, 10.2 (eight up, four down: 10.2).
 // The number sets the order of a row's sums: it goes by kSplitSms, not by the device, and in
 // batch-invariant mode, where it must not go by the number of slots, by k alone.
 int split_of(int64_t K, int bytes, int64_t tiles)
