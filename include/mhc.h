@@ -644,6 +644,8 @@ MHC_API mhc_status mhc_fp8_wgrad(const uint8_t *at, mhc_fp8 format_a, const floa
  * in an order that C, F, T k and E set, in batch-invariant mode C and F alone:
  * the other tokens' values do not matter.
  * T <= 128, k <= 32, C and F multiples of 16 and <= 16384.
+ * Sooner than sort, dispatch, products and combine up to 4 slots an expert (T k / E
+ * where all are used); from 8 on those are.
  * ws: mhc_workspace_bytes(MHC_OP_MOE_FEW_FWD, T, k, C + F). */
 MHC_API mhc_status mhc_moe_few_fwd(const void *x, mhc_dtype dtype, const int32_t *ids,
                                    const float *w, const void *w1, const float *s1, const void *w2,

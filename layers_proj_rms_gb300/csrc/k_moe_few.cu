@@ -25,10 +25,11 @@
 // fp16, two of the values times a power of two that brings the largest of the 32 that a
 // column has in a step to [2^14, 2^15), undone in the fp32 sums: off by 2^-23 of the
 // value or 2^-40 of that largest (unscaled terms overflow at 65504 and are
-// subnormal below 1e-4).  A term more than 16 bits of h need, and sums of their own for each
-// piece (see there), take 199 us for 190 at 13 tokens of 60 experts, 4096 x 1408.  8-bit weights: x and h are quantised by blocks of 128, as
-// mhc_fp8_quant does, when a segment's rows are brought to shared memory; each block's
-// product is scaled into fp32 sums.
+// subnormal below 1e-4).  The splitting, the third term and the sums that each piece has
+// for itself take 199 us for 190 at 13 tokens of 60 experts, 4096 x 1408.  8-bit weights:
+// x and h are quantised by blocks of 128, as mhc_fp8_quant does, when a segment's rows
+// are brought to shared memory; each block's product is scaled into fp32 sums, by a row's
+// scale above 2^88 or below 2^-94 with care (f8_scaled).
 //
 // A slot's row of y is written once and a token's slots are added up in their
 // order, so nothing depends on which block did what.  (The last block at a tile of
