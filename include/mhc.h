@@ -642,7 +642,8 @@ MHC_API mhc_status mhc_fp8_wgrad(const uint8_t *at, mhc_fp8 format_a, const floa
  * and the activation are quantised to e4m3 by blocks of 128 as mhc_fp8_quant
  * does, the latter from its fp32 values.  Each slot's sums are fp32 throughout,
  * in an order that C, F, T k and E set, in batch-invariant mode C and F alone:
- * the other tokens' values do not matter.
+ * the other tokens' values do not matter.  Weights are finite (an infinity in w2 may
+ * give NaN).
  * T <= 128, k <= 32, C and F multiples of 16 and <= 16384.
  * Sooner than sort, dispatch, products and combine up to 4 slots an expert (T k / E
  * where all are used); from 8 on those are.
